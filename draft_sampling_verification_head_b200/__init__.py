@@ -19,6 +19,8 @@ SPEC_ERR_TIMEOUT, SPEC_ERR_WORKSPACE, SPEC_ERR_TOKEN_RANGE = -4, -5, -6
 SPEC_F32, SPEC_BF16 = 0, 1
 SPEC_FLAG_FMA_BIAS = 1
 SPEC_FLAG_TRACE = 2
+SPEC_WORKSPACE_MIN = 256
+SPEC_SCAN_CHUNK = 16
 
 # (name, restype, argtypes) of every exported symbol declared in include/*.h
 _P = ctypes.c_void_p
@@ -39,6 +41,14 @@ _SIGS = {
     "spec_l2_persist": (ctypes.c_int, [_P, ctypes.c_size_t, _P]),
     "spec_schedule_verify_len": (ctypes.c_int, [_P, ctypes.c_int32, ctypes.c_int32, _P,
                                                  ctypes.c_int32, _P, _P]),
+    "spec_embed_workspace_size": (ctypes.c_size_t, [_P]),
+    "spec_embed": (ctypes.c_int, [_P] * 6),
+    "spec_embed_grad": (ctypes.c_int, [_P] * 6),
+    "spec_gated_scan": (ctypes.c_int, [_P] * 10),
+    "spec_gated_scan_grad": (ctypes.c_int, [_P] * 13),
+    "spec_bias_w4": (ctypes.c_int, [_P] * 9),
+    "spec_w4_quantize": (ctypes.c_int, [_P, _P, ctypes.c_int32, _P, _P, _P]),
+    "spec_verify_probs": (ctypes.c_int, [_P] * 13),
     "spec_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "spec_last_launch_count": (ctypes.c_int32, []),
     "spec_debug_philox": (ctypes.c_int, [_P, _P, _P, ctypes.c_int32, _P]),
@@ -54,6 +64,40 @@ class SpecParams(ctypes.Structure):
                 ("seed", ctypes.c_uint64), ("cycle", ctypes.c_uint64),
                 ("spin_limit", ctypes.c_uint64), ("flags", ctypes.c_uint32),
                 ("row_offset", ctypes.c_uint32)]
+
+
+class SpecEmbedParams(ctypes.Structure):
+    """Mirror of spec_embed_params."""
+    _fields_ = [("n", ctypes.c_int32), ("V", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("row_dtype", ctypes.c_int32),
+                ("accumulate", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("table_stride", ctypes.c_int64),
+                ("row_stride", ctypes.c_int64)]
+
+
+class SpecScanParams(ctypes.Structure):
+    """Mirror of spec_scan_params."""
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("gate_stride", ctypes.c_int64),
+                ("x_stride", ctypes.c_int64), ("h_stride", ctypes.c_int64)]
+
+
+class SpecW4Params(ctypes.Structure):
+    """Mirror of spec_w4_params."""
+    _fields_ = [("B", ctypes.c_int32), ("r", ctypes.c_int32), ("V", ctypes.c_int32),
+                ("group", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("scale_dtype", ctypes.c_int32), ("base_dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("x_rows", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("x_stride", ctypes.c_int64),
+                ("base_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64)]
+
+
+class SpecProbsParams(ctypes.Structure):
+    """Mirror of spec_probs_params."""
+    _fields_ = [("B", ctypes.c_int32), ("K", ctypes.c_int32), ("V", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("draft_dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("target_stride", ctypes.c_int64),
+                ("draft_stride", ctypes.c_int64)]
 
 
 _lib = None
@@ -109,6 +153,93 @@ class Params:
                           self.row_offset)
 
 
+_DT = {"f32": SPEC_F32, "bf16": SPEC_BF16}
+
+
+class _Held:
+    """The C structure of a parameter object, made once: the objects are frozen."""
+
+    def c(self):
+        c = self.__dict__.get("_c")
+        if c is None:
+            c = self._make()
+            object.__setattr__(self, "_c", c)
+        return c
+
+
+@dataclass(frozen=True)
+class EmbedParams(_Held):
+    """Sizes of embed / embed_grad (spec_embed_params)."""
+    n: int
+    V: int
+    D: int
+    dtype: str = "bf16"
+    row_dtype: str = "bf16"
+    scale: float = 1.0
+    accumulate: bool = False
+    table_stride: int = 0
+    row_stride: int = 0
+
+    def _make(self):
+        return SpecEmbedParams(self.n, self.V, self.D, _DT[self.dtype], _DT[self.row_dtype],
+                               1 if self.accumulate else 0, float(self.scale), 0,
+                               self.table_stride, self.row_stride)
+
+
+@dataclass(frozen=True)
+class ScanParams(_Held):
+    """Sizes of gated_scan / gated_scan_grad (spec_scan_params)."""
+    B: int
+    T: int
+    D: int
+    dtype: str = "bf16"
+    gate_stride: int = 0
+    x_stride: int = 0
+    h_stride: int = 0
+
+    def _make(self):
+        return SpecScanParams(self.B, self.T, self.D, _DT[self.dtype], self.gate_stride,
+                              self.x_stride, self.h_stride)
+
+
+@dataclass(frozen=True)
+class W4Params(_Held):
+    """Sizes of bias_w4 / w4_quantize (spec_w4_params)."""
+    B: int
+    r: int
+    V: int
+    group: int = 128
+    dtype: str = "bf16"
+    scale_dtype: str = "bf16"
+    base_dtype: str = "bf16"
+    out_dtype: str = "f32"
+    x_rows: int = 0
+    x_stride: int = 0
+    base_stride: int = 0
+    out_stride: int = 0
+
+    def _make(self):
+        return SpecW4Params(self.B, self.r, self.V, self.group, _DT[self.dtype],
+                            _DT[self.scale_dtype], _DT[self.base_dtype], _DT[self.out_dtype],
+                            self.x_rows, 0, self.x_stride, self.base_stride, self.out_stride)
+
+
+@dataclass(frozen=True)
+class ProbsParams(_Held):
+    """Sizes of verify_probs (spec_probs_params)."""
+    B: int
+    K: int
+    V: int
+    dtype: str = "f32"
+    draft_dtype: str = "f32"
+    target_stride: int = 0
+    draft_stride: int = 0
+
+    def _make(self):
+        return SpecProbsParams(self.B, self.K, self.V, _DT[self.dtype], _DT[self.draft_dtype], 0,
+                               self.target_stride, self.draft_stride)
+
+
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -124,11 +255,16 @@ def _check(code, what):
         raise SpecError(code, what)
 
 
-def workspace_size(p: Params) -> int:
+def workspace_size(p) -> int:
+    """Bytes of workspace for the calls these parameters (of any kind) belong to."""
+    if isinstance(p, EmbedParams):
+        return int(lib().spec_embed_workspace_size(ctypes.byref(p.c())))
+    if isinstance(p, (ScanParams, W4Params, ProbsParams)):
+        return SPEC_WORKSPACE_MIN
     return int(lib().spec_workspace_size(ctypes.byref(p.c())))
 
 
-def make_workspace(p: Params, device="cuda"):
+def make_workspace(p, device="cuda"):
     """Allocate and zero a workspace for these parameters (torch memory)."""
     import torch
     n = workspace_size(p)
@@ -248,6 +384,141 @@ def schedule_verify_len(conf, sps):
                                           s.shape[0], kb.ctypes.data, ex.ctypes.data),
            "spec_schedule_verify_len")
     return kb, float(ex[0]), float(ex[1])
+
+
+def _ops(p, named, ws, stream):
+    """Raw pointers of an operator's tensors, after the checks that the C side
+    cannot make: named holds (name, tensor or None, dtype, least number of
+    elements from its first one on).  Tensors and workspace must be on the
+    current device (or the given stream's).  The elements of a tensor must be
+    reachable from its data pointer by the strides the parameters give, so a
+    strided view passes if its storage holds them."""
+    import torch
+    s = stream if stream is not None else torch.cuda.current_stream()
+    dev = s.device_index
+    if dev != torch.cuda.current_device():
+        raise ValueError("the stream belongs to another device than the current one")
+    global _TORCH_DT
+    if _TORCH_DT is None:
+        _TORCH_DT = {"f32": torch.float32, "bf16": torch.bfloat16, "i32": torch.int32,
+                     "u8": torch.uint8}
+    out = [ctypes.byref(p.c())]
+    for name, t, dt, least in named:
+        if t is None:
+            out.append(None)
+            continue
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, the call on cuda:{dev}")
+        if t.dtype is not _TORCH_DT[dt]:
+            raise ValueError(f"{name} is {t.dtype}, expected {dt}")
+        if not t.is_contiguous() and t.stride(-1) != 1:
+            raise ValueError(f"{name}: the elements of a row must be contiguous")
+        if t.numel() < least and (t.untyped_storage().nbytes() // t.element_size()
+                                  - t.storage_offset()) < least:
+            raise ValueError(f"{name} holds {t.numel()} elements, expected {least}")
+        out.append(t.data_ptr())
+    if ws.get_device() != dev or ws.numel() * ws.element_size() < workspace_size(p):
+        raise SpecError(SPEC_ERR_WORKSPACE, "workspace too small or on another device")
+    out.append(ws.data_ptr())
+    out.append(s.cuda_stream)
+    return out
+
+
+_TORCH_DT = None
+
+
+def _span(rows, stride, width):
+    """Elements from the first to the last of `rows` rows, `stride` (0: dense) apart."""
+    return 0 if rows <= 0 else (rows - 1) * (stride or width) + width
+
+
+def embed(p: EmbedParams, table, ids, rows, ws, stream=None):
+    """spec_embed: rows[i] = scale * table[ids[i]] (ids int32; -1 gives zeros)."""
+    a = _ops(p, (("table", table, p.dtype, _span(p.V, p.table_stride, p.D)),
+                 ("ids", ids, "i32", p.n),
+                 ("rows", rows, p.row_dtype, _span(p.n, p.row_stride, p.D))), ws, stream)
+    _check(lib().spec_embed(*a), "spec_embed")
+
+
+def embed_grad(p: EmbedParams, ids, drows, dtable, ws, stream=None):
+    """spec_embed_grad: dtable[v] (+)= scale * sum of drows[i] with ids[i] = v."""
+    a = _ops(p, (("ids", ids, "i32", p.n),
+                 ("drows", drows, p.row_dtype, _span(p.n, p.row_stride, p.D)),
+                 ("dtable", dtable, p.dtype, _span(p.V, p.table_stride, p.D))), ws, stream)
+    _check(lib().spec_embed_grad(*a), "spec_embed_grad")
+
+
+def gated_scan(p: ScanParams, gate, x, h0, len, h, h_last, states, ws, stream=None):
+    """spec_gated_scan: h_t = f_t h_{t-1} + (1 - f_t) x_t, f = sigmoid(gate).
+    h0, len, h, h_last and states may be None."""
+    n, e = p.B * p.T, p.B * p.D
+    a = _ops(p, (("gate", gate, p.dtype, _span(n, p.gate_stride, p.D)),
+                 ("x", x, p.dtype, _span(n, p.x_stride, p.D)), ("h0", h0, "f32", e),
+                 ("len", len, "i32", p.B), ("h", h, p.dtype, _span(n, p.h_stride, p.D)),
+                 ("h_last", h_last, "f32", e),
+                 ("states", states, "f32", -(-p.T // SPEC_SCAN_CHUNK) * e)), ws, stream)
+    _check(lib().spec_gated_scan(*a), "spec_gated_scan")
+
+
+def gated_scan_grad(p: ScanParams, gate, x, h0, len, states, dh, dh_last, dgate, dx, dh0, ws,
+                    stream=None):
+    """spec_gated_scan_grad: the gradients of gate, x and h0 from dh and dh_last.
+    h0, len, dh_last and dh0 may be None; states as gated_scan wrote them."""
+    n, e = p.B * p.T, p.B * p.D
+    a = _ops(p, (("gate", gate, p.dtype, _span(n, p.gate_stride, p.D)),
+                 ("x", x, p.dtype, _span(n, p.x_stride, p.D)), ("h0", h0, "f32", e),
+                 ("len", len, "i32", p.B),
+                 ("states", states, "f32", -(-p.T // SPEC_SCAN_CHUNK) * e),
+                 ("dh", dh, p.dtype, _span(n, p.h_stride, p.D)), ("dh_last", dh_last, "f32", e),
+                 ("dgate", dgate, p.dtype, _span(n, p.gate_stride, p.D)),
+                 ("dx", dx, p.dtype, _span(n, p.x_stride, p.D)), ("dh0", dh0, "f32", e)), ws,
+             stream)
+    _check(lib().spec_gated_scan_grad(*a), "spec_gated_scan_grad")
+
+
+def bias_w4(p: W4Params, x, prev, wq, wscale, base, out, ws, stream=None):
+    """spec_bias_w4: out = base + X . W with W in 4 bits (X[b] = x[prev[b]] or
+    x[b]).  prev and base may be None."""
+    a = _ops(p, (("x", x, p.dtype, _span(p.B if prev is None else p.x_rows, p.x_stride, p.r)),
+                 ("prev", prev, "i32", p.B),
+                 ("wq", wq, "u8", p.V * (-(-p.r // 128) * 64)),
+                 ("wscale", wscale, p.scale_dtype, p.V * (p.r // p.group if p.group > 0 else 0)),
+                 ("base", base, p.base_dtype, _span(p.B, p.base_stride, p.V)),
+                 ("out", out, p.out_dtype, _span(p.B, p.out_stride, p.V))), ws, stream)
+    _check(lib().spec_bias_w4(*a), "spec_bias_w4")
+
+
+def w4_quantize(p: W4Params, W, stream=None):
+    """spec_w4_quantize: (wq, wscale) of a factor W [r, V] (float32 or bfloat16)."""
+    import torch
+    dt = "bf16" if W.dtype is torch.bfloat16 else "f32"
+    n = -(-p.r // 128) * 64
+    wq = torch.empty(p.V, n, dtype=torch.uint8, device=W.device)
+    if p.group < 1 or p.r % p.group:
+        raise SpecError(SPEC_ERR_UNSUPPORTED, "spec_w4_quantize")
+    wscale = torch.empty(p.V, p.r // p.group, device=W.device,
+                         dtype=torch.bfloat16 if p.scale_dtype == "bf16" else torch.float32)
+    ws = torch.empty(SPEC_WORKSPACE_MIN, dtype=torch.uint8, device=W.device)
+    a = _ops(p, (("W", W, dt, p.r * p.V),), ws, stream)
+    if not W.is_contiguous():
+        raise ValueError("W must be contiguous")
+    _check(lib().spec_w4_quantize(a[0], a[1], _DT[dt], wq.data_ptr(), wscale.data_ptr(), a[3]),
+           "spec_w4_quantize")
+    return wq, wscale
+
+
+def verify_probs(p: ProbsParams, target, draft_probs, draft, u_accept, u_draw, verify_len, out,
+                 tau, p_draft, q_draft, ws, stream=None):
+    """spec_verify_probs: verification from probabilities and given uniforms.
+    verify_len, p_draft and q_draft may be None."""
+    bk = p.B * p.K
+    a = _ops(p, (("target", target, p.dtype, _span(bk + p.B, p.target_stride, p.V)),
+                 ("draft_probs", draft_probs, p.draft_dtype, _span(bk, p.draft_stride, p.V)),
+                 ("draft", draft, "i32", bk), ("u_accept", u_accept, "f32", bk),
+                 ("u_draw", u_draw, "f32", p.B), ("verify_len", verify_len, "i32", p.B),
+                 ("out", out, "i32", bk + p.B), ("tau", tau, "i32", p.B),
+                 ("p_draft", p_draft, "f32", bk), ("q_draft", q_draft, "f32", bk)), ws, stream)
+    _check(lib().spec_verify_probs(*a), "spec_verify_probs")
 
 
 def last_launch_count() -> int:

@@ -12,19 +12,12 @@
 
 namespace specdec {
 
-namespace {
-
 thread_local int32_t g_last_launches = 0;
+
+namespace {
 
 constexpr uint64_t kDefaultSpin = 4000000ull;  // polls of ~0.5 us back-off: about 2 s
 constexpr int32_t kMaxLoopCycles = 1 << 16;     // record tags of one launch stay below 2^31
-
-int num_sms() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-  return n;
-}
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -66,6 +59,13 @@ uint8_t* body_of(void* ws) { return reinterpret_cast<uint8_t*>(ws) + sizeof(WsHe
 size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 
 }  // namespace
+
+int num_sms() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  return n;
+}
 
 // W [r, V] bf16: boxes of 64 tokens x box_k rank rows, 128-byte swizzle.
 bool make_tmap_W(CUtensorMap* m, const void* W, int r, int V, int box_k) {

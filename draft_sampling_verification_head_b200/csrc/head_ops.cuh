@@ -1,0 +1,62 @@
+// Interfaces between the entry points of the head's operators (head_api.cu)
+// and their kernels, and the device helpers those share.
+#pragma once
+
+#include "common.cuh"
+
+namespace specdec {
+
+// Record a device-side error of an operator: the first one stays.  Unlike
+// record_error this leaves the abort flag alone, which only the persistent
+// kernels of the cycle poll and reset.
+SPEC_DEV void report_error(WsHeader* h, int32_t code, int32_t site, int32_t a, int32_t b) {
+  if (atomicCAS(&h->status, 0, code) == 0) {
+    h->err_where = site;
+    h->err_a = a;
+    h->err_b = b;
+  }
+}
+
+// Element stores: fp32 as it is, bf16 rounded to nearest even.
+SPEC_DEV void store_f(float* p, int64_t i, float v) { p[i] = v; }
+SPEC_DEV void store_f(__nv_bfloat16* p, int64_t i, float v) { p[i] = __float2bfloat16_rn(v); }
+
+// ---- Scaled lookup and its gradient -------------------------------------------
+size_t embed_grad_ws_bytes(const spec_embed_params& p);
+template <typename TT, typename TR>
+cudaError_t launch_embed(const spec_embed_params& p, const TT* table, const int32_t* ids, TR* rows,
+                         WsHeader* hdr, int num_sms, cudaStream_t st, int* launches);
+template <typename TT, typename TR>
+cudaError_t launch_embed_grad(const spec_embed_params& p, const int32_t* ids, const TR* drows,
+                              TT* dtable, uint8_t* body, WsHeader* hdr, int num_sms,
+                              cudaStream_t st, int* launches);
+
+// ---- Gated linear recurrence and its gradient -------------------------------------
+template <typename T>
+cudaError_t launch_scan(const spec_scan_params& p, const T* gate, const T* x, const float* h0,
+                        const int32_t* len, T* h, float* h_last, float* states, WsHeader* hdr,
+                        int num_sms, cudaStream_t st, int* launches);
+template <typename T>
+cudaError_t launch_scan_grad(const spec_scan_params& p, const T* gate, const T* x, const float* h0,
+                             const int32_t* len, const float* states, const T* dh,
+                             const float* dh_last, T* dgate, T* dx, float* dh0, WsHeader* hdr,
+                             int num_sms, cudaStream_t st, int* launches);
+
+// ---- Vocabulary product with 4-bit weights ------------------------------------------
+template <typename T>
+cudaError_t launch_bias_w4(const spec_w4_params& p, const T* x, const int32_t* prev,
+                           const uint8_t* wq, const void* wscale, const void* base, void* out,
+                           WsHeader* hdr, int num_sms, cudaStream_t st, int* launches);
+template <typename T>
+cudaError_t launch_w4_quantize(const spec_w4_params& p, const T* W, uint8_t* wq, void* wscale,
+                               cudaStream_t st);
+
+// ---- Verification from probabilities ---------------------------------------------------
+template <typename T, typename TD>
+cudaError_t launch_verify_probs(const spec_probs_params& p, const T* target, const TD* draft_probs,
+                                const int32_t* draft, const float* u_accept, const float* u_draw,
+                                const int32_t* verify_len, int32_t* out, int32_t* tau,
+                                float* p_draft, float* q_draft, WsHeader* hdr, int num_sms,
+                                cudaStream_t st, int* launches);
+
+}  // namespace specdec

@@ -285,6 +285,195 @@ spec_status spec_schedule_verify_len(const float *conf, int32_t B, int32_t K,
  * carve-out belongs to this process's context and ends with it. */
 spec_status spec_l2_persist(const void *ptr, size_t bytes, spec_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Operators around the sequential head.  The calls above fuse a head's lookup,
+ * recurrence, vocabulary product and verification into one cycle; these offer
+ * the same steps one by one, in the forms a program needs beside the cycle: a
+ * head that is trained, that runs over long sequences, whose vocabulary factor
+ * is held in 4 bits, or whose draws are made outside the library.  Chained, they
+ * are: tokens -> rows of U (spec_embed) -> gated recurrence (spec_gated_scan)
+ * -> vocabulary product and base logits (spec_bias_w4) -> probabilities ->
+ * spec_verify_probs.  The pages give no counterpart of these forms.
+ *
+ * Rules shared by all of them.  Tensors are row-major device memory of the
+ * current device, rows contiguous, any element alignment (16-byte aligned
+ * pointers and row strides run faster); strides are in elements, 0 = dense.
+ * Outputs may not overlap inputs unless a comment says so.  `workspace` holds
+ * at least SPEC_WORKSPACE_MIN bytes (spec_embed_grad: what
+ * spec_embed_workspace_size returns), zeroed once by spec_workspace_init; errors found
+ * on the device go there and are read by spec_sync_status.  spec_embed_grad
+ * writes all over its workspace, so that one serves no other call; the others
+ * touch only the status and may share any workspace.  All calls can be
+ * captured into a CUDA graph.  No call waits for another CTA's progress, sums
+ * are taken in a fixed order, and equal inputs give equal bits.
+ * ------------------------------------------------------------------------- */
+#define SPEC_WORKSPACE_MIN 256
+
+typedef struct {
+  int32_t n;             /* tokens, >= 0 */
+  int32_t V;             /* rows of the table, >= 1 */
+  int32_t D;             /* row width, 1 .. 65536 */
+  int32_t dtype;         /* spec_dtype of the table (lookup) or of its gradient */
+  int32_t row_dtype;     /* spec_dtype of the rows: the lookup's output, the gradient's input */
+  int32_t accumulate;    /* gradient: 0 = write the whole table gradient, 1 = add to it */
+  float scale;           /* finite */
+  int32_t reserved;      /* 0 */
+  int64_t table_stride;  /* between table rows; 0 = D */
+  int64_t row_stride;    /* between rows; 0 = D */
+} spec_embed_params;
+
+/* Bytes of workspace spec_embed_grad needs (0 if the parameters are invalid);
+ * enough for spec_embed too. */
+size_t spec_embed_workspace_size(const spec_embed_params *p);
+
+/* Scaled lookup, the head's U[prev] by itself: rows[i] = scale * table[ids[i]],
+ * multiplied in fp32 and rounded once.  ids [n] int32; -1 ("no token", as in
+ * the outputs of the cycle) gives a row of zeros, any other id outside [0, V)
+ * too, and is reported as SPEC_ERR_TOKEN_RANGE. */
+spec_status spec_embed(const spec_embed_params *p, const void *table, const int32_t *ids,
+                       void *rows, void *workspace, spec_stream_t stream);
+
+/* Its gradient: dtable[v] (+)= scale * sum of drows[i] over the i with
+ * ids[i] = v.  The tokens are sorted first, so each table row is written once,
+ * by fp32 sums in a fixed order (ascending i, in pieces joined in order), rounded once.  With
+ * accumulate = 0 every table row is written (rows no token names become 0);
+ * with 1 only the rows named by a token are touched.  Ids outside [0, V) add
+ * nothing; all but -1 are reported as SPEC_ERR_TOKEN_RANGE. */
+spec_status spec_embed_grad(const spec_embed_params *p, const int32_t *ids, const void *drows,
+                            void *dtable, void *workspace, spec_stream_t stream);
+
+#define SPEC_SCAN_CHUNK 16 /* steps between two states kept for the gradient */
+
+typedef struct {
+  int32_t B;            /* sequences, >= 1 */
+  int32_t T;            /* steps, >= 0 */
+  int32_t D;            /* channels, >= 1 */
+  int32_t dtype;        /* spec_dtype of gate, x, h and their gradients; states are float */
+  int64_t gate_stride;  /* between the steps of gate and dgate; 0 = D; sequences are T steps apart */
+  int64_t x_stride;     /* the same of x and dx */
+  int64_t h_stride;     /* the same of h and dh */
+} spec_scan_params;
+
+/* Gated linear recurrence over sequences, a sequential head that trains by a
+ * scan (beside spec_cycle_rnn's, which is sequential by its form):
+ *   f_t = sigmoid(gate_t),  h_t = f_t h_{t-1} + (1 - f_t) x_t,  h_{-1} = h0.
+ *   gate, x  [B, T, D] dtype
+ *   h0       [B, D] float, or NULL (zeros)
+ *   len      [B] int32, or NULL (all T): steps t >= len[b] do not belong to
+ *            sequence b; h is left as it was there.  A length outside 0..T is
+ *            clamped and reported as SPEC_ERR_INVALID_ARG.
+ *   h        [B, T, D] dtype, or NULL
+ *   h_last   [B, D] float, or NULL: the state after the last step (h0 where
+ *            len is 0); may be the buffer of h0, as in step-by-step decoding
+ *   states   [B, ceil(T / SPEC_SCAN_CHUNK), D] float, or NULL: the state before
+ *            every SPEC_SCAN_CHUNK-th step, which the gradient needs (past the
+ *            end of a sequence: its last state)
+ * States are carried in fp32. */
+spec_status spec_gated_scan(const spec_scan_params *p, const void *gate, const void *x,
+                            const float *h0, const int32_t *len, void *h, float *h_last,
+                            float *states, void *workspace, spec_stream_t stream);
+
+/* Its gradient, given dh [B, T, D] (dtype) of h and dh_last [B, D] (float, or
+ * NULL) of h_last:
+ *   delta_t = dh_t + f_{t+1} delta_{t+1}, dh_last added at the last step,
+ *   dx_t = (1 - f_t) delta_t,  dgate_t = delta_t (h_{t-1} - x_t) f_t (1 - f_t),
+ *   dh0 = f_0 delta_0 (dh_last where len is 0).
+ * h_{t-1} is computed again in fp32 from `states`, as the forward call wrote
+ * them for the same inputs.  dgate and dx are written over all T steps, with
+ * zeros where t >= len[b]; dh is not read there.  dh0 may be NULL. */
+spec_status spec_gated_scan_grad(const spec_scan_params *p, const void *gate, const void *x,
+                                 const float *h0, const int32_t *len, const float *states,
+                                 const void *dh, const float *dh_last, void *dgate, void *dx,
+                                 float *dh0, void *workspace, spec_stream_t stream);
+
+typedef struct {
+  int32_t B;            /* rows, >= 1 (fast up to 16) */
+  int32_t r;            /* features, a multiple of group, up to 65536 */
+  int32_t V;            /* vocabulary, >= 1 */
+  int32_t group;        /* features that share a scale: 32, 64 or 128 */
+  int32_t dtype;        /* spec_dtype of x */
+  int32_t scale_dtype;  /* spec_dtype of wscale */
+  int32_t base_dtype;   /* spec_dtype of base */
+  int32_t out_dtype;    /* spec_dtype of out */
+  int32_t x_rows;       /* rows of x when prev is given */
+  int32_t reserved;     /* 0 */
+  int64_t x_stride;     /* between rows of x; 0 = r */
+  int64_t base_stride;  /* between rows of base; 0 = V */
+  int64_t out_stride;   /* between rows of out; 0 = V */
+} spec_w4_params;
+
+/* Vocabulary product with the factor W in 4 bits:
+ *   out[b, v] = base[b, v] + sum_k X[b, k] * (code[v, k] - 8) * wscale[v, k / group],
+ * X[b] = x[prev[b]] (the Markov bias of spec_markov_bias) or, with prev NULL,
+ * x[b].  Products and the sum inside a group are exact or fp32, groups are
+ * added in fp32 in a fixed order; out is rounded once.
+ *   x       [B, r], or [x_rows, r] with prev; dtype
+ *   prev    [B] int32, or NULL; an id outside [0, x_rows) is clamped and
+ *           reported as SPEC_ERR_TOKEN_RANGE
+ *   wq      [V, R/2] bytes, R = r rounded up to a multiple of 128; 16-byte
+ *           aligned.  Two codes (0..15) a byte, the lower feature in the lower
+ *           half; in each run of 128 features (64 bytes) the sixteen 4-byte
+ *           words w = 0..15 stand in the order 4 (w mod 4) + floor(w / 4), so
+ *           that 16 consecutive bytes hold one word of each 32 features;
+ *           features past r hold code 8
+ *   wscale  [V, r / group], scale_dtype
+ *   base    [B, V] base_dtype, or NULL
+ *   out     [B, V] out_dtype; may be base where type and stride are the same */
+spec_status spec_bias_w4(const spec_w4_params *p, const void *x, const int32_t *prev,
+                         const void *wq, const void *wscale, const void *base, void *out,
+                         void *workspace, spec_stream_t stream);
+
+/* Lay a factor W [r, V] (dtype w_dtype, as for spec_markov_bias) out for
+ * spec_bias_w4: per token and group, scale = max |W| / 7 rounded to
+ * scale_dtype, code = 8 + W / scale rounded to nearest even and clamped to
+ * 0..15 (8 where the scale is 0; a NaN counts as 0).  Uses r, V, group and
+ * scale_dtype of p.  wq and wscale are outputs of the sizes above. */
+spec_status spec_w4_quantize(const spec_w4_params *p, const void *W, int32_t w_dtype, void *wq,
+                             void *wscale, spec_stream_t stream);
+
+typedef struct {
+  int32_t B;              /* batch rows, >= 1 */
+  int32_t K;              /* block length, 1 .. 1024 */
+  int32_t V;              /* vocabulary, >= 1 */
+  int32_t dtype;          /* spec_dtype of target */
+  int32_t draft_dtype;    /* spec_dtype of draft_probs */
+  int32_t reserved;       /* 0 */
+  int64_t target_stride;  /* between vocabulary rows of target; 0 = V */
+  int64_t draft_stride;   /* between vocabulary rows of draft_probs; 0 = V */
+} spec_probs_params;
+
+/* Verification of drafted tokens against the target's probabilities from given
+ * random numbers: the rule of spec_verify_block for programs that hold
+ * probabilities (after penalties or truncation, not softmax of logits) and
+ * draw their own uniforms.
+ *   target      [B, K+1, V]  dtype        p, row K = bonus row
+ *   draft_probs [B, K, V]    draft_dtype  q
+ *   draft       [B, K]       int32
+ *   u_accept    [B, K]       float        uniforms in [0, 1)
+ *   u_draw      [B]          float
+ *   verify_len  [B]          int32, or NULL (all K): K_b in 0..K; 0 draws from
+ *               row 0 (plain decoding); a negative length marks a row to skip,
+ *               of which nothing is read or written; one above K is clamped
+ *               and reported as SPEC_ERR_INVALID_ARG
+ *   out [B, K+1], tau [B] int32; p_draft, q_draft [B, K] float or NULL, as
+ *   for spec_verify_block (NaN past the positions whose test ran)
+ * Position i is accepted iff u_accept * q_i(d_i) < p_i(d_i), compared exactly.
+ * The draw takes the first token whose inclusive mass exceeds u_draw * total
+ * (else the last one with mass), in ascending token order, from max(p_j - q_j, 0)
+ * at the first rejection j (p_j where that has no mass), or from p_{K_b}.
+ * Masses are summed in 64 bits, so the token does not hang on the order of the
+ * sums.  A probability that is NaN, infinite or negative counts as 0.  A row
+ * without any mass emits -1 there, has tau = the number of accepted drafts,
+ * and is reported as SPEC_ERR_INVALID_ARG.  A draft outside [0, V) is rejected
+ * and reported as SPEC_ERR_TOKEN_RANGE.  Only the rows of the first rejection
+ * (or the bonus row) are read whole. */
+spec_status spec_verify_probs(const spec_probs_params *p, const void *target,
+                              const void *draft_probs, const int32_t *draft,
+                              const float *u_accept, const float *u_draw,
+                              const int32_t *verify_len, int32_t *out, int32_t *tau,
+                              float *p_draft, float *q_draft, void *workspace,
+                              spec_stream_t stream);
+
 /* Synchronise `stream` and return the device-side status recorded in the
  * workspace by the calls issued on it (SPEC_OK if none failed). */
 spec_status spec_sync_status(const void *workspace, spec_stream_t stream);
