@@ -1,20 +1,29 @@
 // Gated linear recurrence over sequences, h_t = f_t h_{t-1} + (1 - f_t) x_t
 // with f = sigmoid(gate), and its gradient.
+//
+// A step is the affine map h -> f h + z, z = (1 - f) x, and maps compose:
+// (f2, z2) after (f1, z1) is (f1 f2, f2 z1 + z2).  So a long sequence is cut
+// into pieces of kChunk steps, one per warp, which are reduced to one map per
+// channel each while their f and z stay in registers; the maps are joined in
+// time order (warps of a CTA through shared memory, CTAs of a cluster through
+// each other's shared memory), which gives every piece the state it starts
+// from, and the pieces are run once more from there.  Inputs are read once and
+// outputs written once, whatever the length; equal inputs give equal bits since
+// the joins are taken in a fixed order.
+#include <cooperative_groups.h>
+
+#include <type_traits>
+
 #include "head_ops.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace specdec {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kChunk = SPEC_SCAN_CHUNK;
-
-// f = sigmoid(g) and i = 1 - f = sigmoid(-g), each to fp32 accuracy.
-SPEC_DEV void gate_of(float g, float& f, float& i) {
-  const float e = expf(-fabsf(g));  // in (0, 1]
-  const float big = 1.f / (1.f + e), small = e * big;
-  f = g >= 0.f ? big : small;
-  i = g >= 0.f ? small : big;
-}
+constexpr int kChunk = SPEC_SCAN_CHUNK;  // steps per piece
+constexpr int kMaxCluster = 8;           // CTAs per cluster (portable limit)
+constexpr int kSoloWarps = 8;            // warps per CTA where each has a job of its own
 
 SPEC_DEV int len_of(const int32_t* len, int b, int T, WsHeader* hdr, bool say) {
   if (!len) return T;
@@ -24,98 +33,570 @@ SPEC_DEV int len_of(const int32_t* len, int b, int T, WsHeader* hdr, bool say) {
   return n < 0 ? 0 : T;
 }
 
-// One thread per channel, step by step.
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
-    k_scan(spec_scan_params p, const T* __restrict__ gate, const T* __restrict__ x,
-           const float* h0, const int32_t* __restrict__ len, T* h, float* h_last, float* states,
-           WsHeader* hdr) {
-  const int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (e >= (int64_t)p.B * p.D) return;
-  const int b = (int)(e / p.D), c = (int)(e % p.D);
-  const int n = len_of(len, b, p.T, hdr, c == 0);
-  const int nch = (p.T + kChunk - 1) / kChunk;
-  float s = h0 ? h0[e] : 0.f;
-  for (int t = 0; t < p.T; ++t) {
-    if (states && t % kChunk == 0) states[((int64_t)b * nch + t / kChunk) * p.D + c] = s;
-    if (t >= n) continue;
-    const int64_t row = (int64_t)b * p.T + t;
-    float f, i;
-    gate_of(load_f(gate, row * p.gate_stride + c), f, i);
-    s = fmaf(f, s, i * load_f(x, row * p.x_stride + c));
-    if (h) store_f(h, row * p.h_stride + c, s);
+// ----------------------------------------------------------------------------
+// V fp32 values of one thread: V = 2 in one 64-bit register on the packed pipe
+// (each lane rounded exactly like the scalar operation), which halves the issue
+// slots that bound these kernels.
+// ----------------------------------------------------------------------------
+template <int V>
+struct Vec;
+template <>
+struct Vec<1> {
+  float v;
+  SPEC_DEV static Vec all(float a) { return {a}; }
+  SPEC_DEV float get(int) const { return v; }
+  SPEC_DEV friend Vec operator+(Vec a, Vec b) { return {a.v + b.v}; }
+  SPEC_DEV friend Vec operator*(Vec a, Vec b) { return {a.v * b.v}; }
+  SPEC_DEV friend Vec fma(Vec a, Vec b, Vec c) { return {fmaf(a.v, b.v, c.v)}; }
+  template <typename F>
+  SPEC_DEV Vec map(F f) const { return {f(v)}; }
+};
+template <>
+struct Vec<2> {
+  uint64_t v;
+  SPEC_DEV static Vec of(float a, float b) {
+    Vec r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
   }
-  if (h_last) h_last[e] = s;
+  SPEC_DEV static Vec all(float a) { return of(a, a); }
+  SPEC_DEV float get(int k) const {
+    float a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+    return k ? b : a;
+  }
+  SPEC_DEV friend Vec operator+(Vec a, Vec b) {
+    Vec r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+  }
+  SPEC_DEV friend Vec operator*(Vec a, Vec b) {
+    Vec r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+  }
+  SPEC_DEV friend Vec fma(Vec a, Vec b, Vec c) {
+    Vec r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+  }
+  template <typename F>
+  SPEC_DEV Vec map(F f) const { return of(f(get(0)), f(get(1))); }
+};
+
+// V channels of one step as they lie in memory: a float, two bf16, or a single
+// bf16 where width or alignment leave no pairs or channels are few.
+template <typename T, int V>
+using RawOf = std::conditional_t<std::is_same<T, float>::value || V == 2, uint32_t, uint16_t>;
+
+template <typename T, int V>
+SPEC_DEV Vec<V> raw_value(RawOf<T, V> r) {
+  if constexpr (std::is_same<T, float>::value)
+    return {__uint_as_float(r)};
+  else if constexpr (V == 2)
+    return Vec<2>::of(__uint_as_float(r << 16), __uint_as_float(r & 0xFFFF0000u));
+  else
+    return {__uint_as_float((uint32_t)r << 16)};
+}
+template <typename T, int V>
+SPEC_DEV void raw_store(T* p, Vec<V> x) {
+  if constexpr (std::is_same<T, float>::value)
+    *p = x.get(0);
+  else if constexpr (V == 2)
+    *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(x.get(0), x.get(1));
+  else
+    *p = __float2bfloat16_rn(x.get(0));
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
-    k_scan_grad(spec_scan_params p, const T* __restrict__ gate, const T* __restrict__ x,
-                const int32_t* __restrict__ len, const float* __restrict__ states,
-                const T* __restrict__ dh, const float* dh_last, T* dgate, T* dx, float* dh0,
-                WsHeader* hdr) {
-  const int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (e >= (int64_t)p.B * p.D) return;
-  const int b = (int)(e / p.D), c = (int)(e % p.D);
-  const int n = len_of(len, b, p.T, hdr, c == 0);
-  const int nch = (p.T + kChunk - 1) / kChunk;
-  float carry = dh_last ? dh_last[e] : 0.f;
-  for (int ch = nch - 1; ch >= 0; --ch) {
-    const int t0 = ch * kChunk;
-    float s = states[((int64_t)b * nch + ch) * p.D + c];
-    float f[kChunk], i[kChunk], u[kChunk];
+// f = sigmoid(g) = 1 / (1 + e), i = 1 - f = e f with e = exp(-g), so neither is
+// found by cancellation.  g is clamped to [-87, 100], where e stays a number
+// and f, i are 0 and 1 to fp32's range; a NaN passes.  e = 2^t (1 + d) where t
+// is -g log2(e) rounded to fp32 and d makes up for that rounding, which for
+// large |g| would cost more than the rest together.
+template <typename T, int V>
+SPEC_DEV void gate_of(RawOf<T, V> raw, Vec<V>& f, Vec<V>& i) {
+  constexpr float kLn2 = 0.69314718056f;
+  Vec<V> t, d;
+  if constexpr (std::is_same<T, float>::value) {
+    float g = __uint_as_float(raw);
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(g) : "f"(g), "f"(-87.f));
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(g) : "f"(g), "f"(100.f));
+    constexpr float kL = 1.44269504089f;
+    t.v = g * -kL;
+    d.v = fmaf(g, -kL, -t.v) * kLn2;
+  } else {
+    // bf16 has 8 significant bits: with the upper 16 of log2(e) the product is
+    // exact, and the lower ones give d
+    constexpr float kHi = 1.44268798828125f;  // 47274 / 2^15
+    constexpr float kLo = (float)(1.4426950408889634 - 47274.0 / 32768.0);
+    uint32_t g2 = raw;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(g2) : "r"(g2), "r"(0xC2AEC2AEu));  // -87
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(g2) : "r"(g2), "r"(0x42C842C8u));  // 100
+    const Vec<V> g = raw_value<T, V>((RawOf<T, V>)g2);
+    t = g * Vec<V>::all(-kHi);
+    d = g * Vec<V>::all(-kLo * kLn2);
+  }
+  Vec<V> e = t.map([](float x) { return fexp2(x); });
+  e = fma(e, d, e);
+  f = (e + Vec<V>::all(1.f)).map([](float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+  });
+  i = e * f;
+}
+
+struct ScanArgs {
+  spec_scan_params p;
+  const void* gate;
+  const void* x;
+  const float* h0;
+  const int32_t* len;
+  void* h;
+  float* h_last;
+  float* states;
+  const void* dh;
+  const float* dh_last;
+  void* dgate;
+  void* dx;
+  float* dh0;
+  WsHeader* hdr;
+  int tiles;    // channel tiles per sequence
+  int cluster;  // CTAs per cluster
+  int wide;     // rows lie on 16-byte boundaries
+  int jobs;     // sequences x tiles
+};
+
+// One piece of one input in shared memory, written by 16-byte asynchronous
+// copies where rows allow (zero-filled behind the end), else by plain loads.
+template <typename T, int V>
+struct alignas(16) Piece {
+  RawOf<T, V> at[kChunk][32];
+};
+
+// Steps t .. t + kChunk - 1 of the lane's tile; `left` of them exist.
+template <typename T, int V>
+SPEC_DEV void fetch(Piece<T, V>& dst, const T* src, int64_t stride, int left, int channels,
+                    bool wide) {
+  const int lane = threadIdx.x & 31;
+  if (wide) {
+    constexpr int kEach = 16 / sizeof(T);           // channels per copy
+    constexpr int kPer = 32 * V / kEach;            // copies per step
+    constexpr int kSteps = 32 / kPer;               // steps per instruction
+    const int c = (lane % kPer) * kEach, k0 = lane / kPer;
+#pragma unroll
+    for (int k = 0; k < kChunk; k += kSteps) {
+      const bool in = k + k0 < left && c < channels;
+      const T* s = in ? src + (int64_t)(k + k0) * stride + c : src;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                       smem_u32(&dst.at[k + k0][0]) + c * (uint32_t)sizeof(T)),
+                   "l"(s), "r"(in ? 16 : 0)
+                   : "memory");
+    }
+  } else {
+    RawOf<T, V> r[kChunk];
+#pragma unroll
+    for (int k = 0; k < kChunk; ++k)
+      r[k] = k < left && lane * V < channels
+                 ? __ldg(reinterpret_cast<const RawOf<T, V>*>(src + k * stride + lane * V))
+                 : RawOf<T, V>(0);
+#pragma unroll
+    for (int k = 0; k < kChunk; ++k) dst.at[k][lane] = r[k];
+  }
+}
+
+// Joins the maps of a window's W pieces in each of `cluster` CTAs.  (a, c) is
+// the calling warp's map; warps and ranks are numbered in the order of the
+// recurrence.  carry holds the value before the window in every thread and
+// becomes the one after it; `before` is the one before the calling warp's
+// piece.  The slots alternate between windows, so a window needs one barrier of
+// the CTA and, in a cluster, one of the cluster.
+template <int V, int W>
+struct Joiner {
+  float2 piece[2][W][32 * V];
+  float2 cta[2][kMaxCluster][32 * V];
+};
+template <int V>
+struct Joiner<V, 1> {};
+
+template <int V, int W>
+SPEC_DEV void join(Joiner<V, W>& sm, int par, int warp, int rank, int cluster, Vec<V> a, Vec<V> c,
+                   Vec<V>& carry, Vec<V>& before) {
+  if constexpr (W == 1) {
+    before = carry;
+    carry = fma(a, carry, c);
+  } else {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      sm.piece[par][warp][v * 32 + lane] = make_float2(a.get(v), c.get(v));
+    __syncthreads();
+    float out_b[V], out_c[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float ta = 1.f, tc = 0.f, pa = 1.f, pc = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        if (w == warp) {
+          pa = ta;
+          pc = tc;
+        }
+        const float2 m = sm.piece[par][w][v * 32 + lane];
+        ta *= m.x;
+        tc = fmaf(m.x, tc, m.y);
+      }
+      if (cluster > 1) {
+        if (warp < cluster) {  // the warps hand the CTA's map to one CTA each
+          Joiner<V, W>* far = cg::this_cluster().map_shared_rank(&sm, warp);
+          far->cta[par][rank][v * 32 + lane] = make_float2(ta, tc);
+        }
+        out_b[v] = pa;
+        out_c[v] = pc;
+      } else {
+        out_b[v] = fmaf(pa, carry.get(v), pc);
+        out_c[v] = fmaf(ta, carry.get(v), tc);
+      }
+    }
+    if (cluster > 1) {
+      cg::this_cluster().sync();
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        float s = carry.get(v), mine = s;
+        for (int r = 0; r < cluster; ++r) {
+          if (r == rank) mine = s;
+          const float2 m = sm.cta[par][r][v * 32 + lane];
+          s = fmaf(m.x, s, m.y);
+        }
+        out_b[v] = fmaf(out_b[v], mine, out_c[v]);
+        out_c[v] = s;
+      }
+    }
+    if constexpr (V == 2) {
+      before = Vec<2>::of(out_b[0], out_b[1]);
+      carry = Vec<2>::of(out_c[0], out_c[1]);
+    } else {
+      before = {out_b[0]};
+      carry = {out_c[0]};
+    }
+  }
+}
+
+template <int V>
+SPEC_DEV Vec<V> state_load(const float* p, bool on) {
+  if constexpr (V == 2)
+    return on ? Vec<2>::of(p[0], p[1]) : Vec<2>::all(0.f);
+  else
+    return {on ? p[0] : 0.f};
+}
+template <int V>
+SPEC_DEV void state_store(float* p, Vec<V> x) {
+#pragma unroll
+  for (int v = 0; v < V; ++v) p[v] = x.get(v);
+}
+
+// Forward.  W > 1: a cluster per job (a sequence's tile of 32 V channels) walks
+// the steps in windows of cluster * W pieces.  W = 1: a warp per job, a window is
+// one piece and nothing is joined.  The next window's inputs are requested
+// before the current one is joined.
+template <typename T, int V, int W>
+struct ScanShared {
+  Joiner<V, W> joiner;
+  Piece<T, V> gate[W == 1 ? kSoloWarps : W], x[W == 1 ? kSoloWarps : W];
+};
+
+template <typename T, int V, int W>
+__global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), W == 16 ? 1 : 2)
+    k_scan(ScanArgs a) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  ScanShared<T, V, W>& sm = *reinterpret_cast<ScanShared<T, V, W>*>(smem_raw);
+  const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int C = W == 1 ? 1 : a.cluster, rank = blockIdx.x % C, warp = W == 1 ? 0 : wid;
+  const int job = W == 1 ? blockIdx.x * kSoloWarps + wid : blockIdx.x / C;
+  if (job >= a.jobs) return;  // W = 1 only: whole warps, and no barrier follows
+  const int b = job / a.tiles, ct = (job % a.tiles) * (32 * V), c = ct + lane * V;
+  const int D = a.p.D, Tn = a.p.T;
+  const bool on = c < D;  // pairs are only taken where D is even
+  const int n = len_of(a.len, b, Tn, a.hdr, ct == 0 && rank == 0 && warp == 0 && lane == 0);
+  const int64_t row0 = (int64_t)b * Tn;
+  const T* gp = (const T*)a.gate + row0 * a.p.gate_stride + ct;
+  const T* xp = (const T*)a.x + row0 * a.p.x_stride + ct;
+  T* hp = (T*)a.h + row0 * a.p.h_stride + c;
+  const int nch = (Tn + kChunk - 1) / kChunk;
+  Vec<V> carry = state_load<V>(a.h0 + (int64_t)b * D + c, a.h0 && on);
+
+  const int window = C * W * kChunk;
+  int t0 = (rank * W + warp) * kChunk;
+  auto request = [&](int t) {
+    if (t < n) {
+      fetch(sm.gate[wid], gp + (int64_t)t * a.p.gate_stride, a.p.gate_stride, n - t, D - ct, a.wide);
+      fetch(sm.x[wid], xp + (int64_t)t * a.p.x_stride, a.p.x_stride, n - t, D - ct, a.wide);
+    }
+    cp_async_commit();
+  };
+  request(t0);
+  if (C > 1) cg::this_cluster().sync();  // every CTA runs before another writes to it
+  const int nwin = (Tn + window - 1) / window;
+  for (int win = 0; win < nwin; ++win, t0 += window) {
+    Vec<V> f[kChunk], z[kChunk], ma = Vec<V>::all(1.f), mc = Vec<V>::all(0.f);
+    cp_async_wait<0>();
+    __syncwarp();
+    const int left = n - t0;  // steps of the piece that belong to the sequence
 #pragma unroll
     for (int k = 0; k < kChunk; ++k) {
-      if (t0 + k < n) {
-        const int64_t row = (int64_t)b * p.T + t0 + k;
-        gate_of(load_f(gate, row * p.gate_stride + c), f[k], i[k]);
-        const float xv = load_f(x, row * p.x_stride + c);
-        u[k] = s - xv;
-        s = fmaf(f[k], s, i[k] * xv);
+      gate_of<T, V>(sm.gate[wid].at[k][lane], f[k], z[k]);
+      z[k] = z[k] * raw_value<T, V>(sm.x[wid].at[k][lane]);
+    }
+    if (left < kChunk) {  // the others leave the state as it is
+#pragma unroll
+      for (int k = 0; k < kChunk; ++k)
+        if (k >= left) {
+          f[k] = Vec<V>::all(1.f);
+          z[k] = Vec<V>::all(0.f);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kChunk; ++k) {
+      ma = ma * f[k];
+      mc = fma(f[k], mc, z[k]);
+    }
+    __syncwarp();
+    request(t0 + window);
+    Vec<V> s;
+    join<V, W>(sm.joiner, win & 1, warp, rank, C, ma, mc, carry, s);
+    if (on && a.states && t0 < Tn)
+      state_store<V>(a.states + ((int64_t)b * nch + t0 / kChunk) * D + c, s);
+    if (on && a.h && left > 0) {
+      T* h = hp + (int64_t)t0 * a.p.h_stride;
+#pragma unroll
+      for (int k = 0; k < kChunk; ++k) {
+        s = fma(f[k], s, z[k]);
+        if (k < left) raw_store<T, V>(h, s);
+        h += a.p.h_stride;
       }
+    }
+    __syncwarp();
+  }
+  if (a.h_last && rank == 0 && warp == 0 && on)
+    state_store<V>(a.h_last + (int64_t)b * D + c, carry);
+}
+
+// Gradient.  The state before each piece comes from `states`, so its h are run
+// forward again inside the warp; what is joined, last piece first, are the maps
+// of the reversed recurrence carry -> f (dh + carry).
+template <typename T, int V, int W>
+struct GradShared {
+  Joiner<V, W> joiner;
+  Piece<T, V> gate[W == 1 ? kSoloWarps : W], x[W == 1 ? kSoloWarps : W];
+  Piece<T, V> dh[2][W == 1 ? kSoloWarps : W];  // read again after the join
+};
+
+template <typename T, int V, int W>
+__global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), W == 16 ? 1 : 2)
+    k_scan_grad(ScanArgs a) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  GradShared<T, V, W>& sm = *reinterpret_cast<GradShared<T, V, W>*>(smem_raw);
+  // pieces are numbered from the end: piece 0 of window 0 holds the last steps
+  const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int C = W == 1 ? 1 : a.cluster, rank = blockIdx.x % C, warp = W == 1 ? 0 : wid;
+  const int job = W == 1 ? blockIdx.x * kSoloWarps + wid : blockIdx.x / C;
+  if (job >= a.jobs) return;  // W = 1 only: whole warps, and no barrier follows
+  const int b = job / a.tiles, ct = (job % a.tiles) * (32 * V), c = ct + lane * V;
+  const int D = a.p.D, Tn = a.p.T;
+  const bool on = c < D;
+  const int n = len_of(a.len, b, Tn, a.hdr, ct == 0 && rank == 0 && warp == 0 && lane == 0);
+  const int64_t row0 = (int64_t)b * Tn;
+  const T* gp = (const T*)a.gate + row0 * a.p.gate_stride + ct;
+  const T* xp = (const T*)a.x + row0 * a.p.x_stride + ct;
+  const T* dp = (const T*)a.dh + row0 * a.p.h_stride + ct;
+  T* dgp = (T*)a.dgate + row0 * a.p.gate_stride + c;
+  T* dxp = (T*)a.dx + row0 * a.p.x_stride + c;
+  const int nch = (Tn + kChunk - 1) / kChunk;
+  Vec<V> carry = state_load<V>(a.dh_last + (int64_t)b * D + c, a.dh_last && on);
+
+  const int window = C * W;  // in pieces
+  int ch = nch - 1 - (rank * W + warp);
+  Vec<V> s0;
+  auto request = [&](int q, int par) {
+    const int t = q * kChunk;
+    if (q >= 0 && t < n) {
+      fetch(sm.gate[wid], gp + (int64_t)t * a.p.gate_stride, a.p.gate_stride, n - t, D - ct, a.wide);
+      fetch(sm.x[wid], xp + (int64_t)t * a.p.x_stride, a.p.x_stride, n - t, D - ct, a.wide);
+      fetch(sm.dh[par][wid], dp + (int64_t)t * a.p.h_stride, a.p.h_stride, n - t, D - ct, a.wide);
+    }
+    cp_async_commit();
+    s0 = state_load<V>(a.states + ((int64_t)b * nch + q) * D + c, on && q >= 0);
+  };
+  request(ch, 0);
+  if (C > 1) cg::this_cluster().sync();  // every CTA runs before another writes to it
+  const int nwin = (nch + window - 1) / window;
+  for (int win = 0; win < nwin; ++win, ch -= window) {
+    const int t0 = ch * kChunk, left = ch < 0 ? 0 : n - t0, par = win & 1;
+    Vec<V> f[kChunk], i[kChunk], w[kChunk], ma = Vec<V>::all(1.f), mc = Vec<V>::all(0.f);
+    cp_async_wait<0>();
+    __syncwarp();
+    Vec<V> s = s0;
+#pragma unroll
+    for (int k = 0; k < kChunk; ++k) {
+      gate_of<T, V>(sm.gate[wid].at[k][lane], f[k], i[k]);
+      const Vec<V> x = raw_value<T, V>(sm.x[wid].at[k][lane]);
+      w[k] = fma(x, Vec<V>::all(-1.f), s) * (f[k] * i[k]);
+      s = fma(f[k], s, i[k] * x);
+    }
+    if (left < kChunk) {
+#pragma unroll
+      for (int k = 0; k < kChunk; ++k)
+        if (k >= left) {  // not a step of the sequence: the carry passes, no gradient
+          f[k] = Vec<V>::all(1.f);
+          i[k] = w[k] = Vec<V>::all(0.f);
+          sm.dh[par][wid].at[k][lane] = RawOf<T, V>(0);
+        }
     }
 #pragma unroll
     for (int k = kChunk - 1; k >= 0; --k) {
-      if (t0 + k >= p.T) continue;
-      const int64_t row = (int64_t)b * p.T + t0 + k;
-      float dg = 0.f, dxv = 0.f;
-      if (t0 + k < n) {
-        const float delta = carry + load_f(dh, row * p.h_stride + c);
-        dxv = delta * i[k];
-        dg = dxv * u[k] * f[k];
-        carry = delta * f[k];
-      }
-      store_f(dgate, row * p.gate_stride + c, dg);
-      store_f(dx, row * p.x_stride + c, dxv);
+      ma = ma * f[k];
+      mc = f[k] * (mc + raw_value<T, V>(sm.dh[par][wid].at[k][lane]));
     }
+    __syncwarp();
+    request(ch - window, par ^ 1);
+    join<V, W>(sm.joiner, par, warp, rank, C, ma, mc, carry, s);
+    if (on && ch >= 0) {
+      const int rows = min(kChunk, Tn - t0);
+      T* dg = dgp + (int64_t)(t0 + kChunk - 1) * a.p.gate_stride;
+      T* dx = dxp + (int64_t)(t0 + kChunk - 1) * a.p.x_stride;
+#pragma unroll
+      for (int k = kChunk - 1; k >= 0; --k) {
+        const Vec<V> delta = s + raw_value<T, V>(sm.dh[par][wid].at[k][lane]);
+        if (k < left) {
+          raw_store<T, V>(dg, delta * w[k]);
+          raw_store<T, V>(dx, delta * i[k]);
+        } else if (k < rows) {
+          raw_store<T, V>(dg, Vec<V>::all(0.f));
+          raw_store<T, V>(dx, Vec<V>::all(0.f));
+        }
+        s = delta * f[k];
+        dg -= a.p.gate_stride;
+        dx -= a.p.x_stride;
+      }
+    }
+    __syncwarp();
   }
-  if (dh0) dh0[e] = carry;
+  if (a.dh0 && rank == 0 && warp == 0 && on)
+    state_store<V>(a.dh0 + (int64_t)b * D + c, carry);
 }
 
-int grid_of(const spec_scan_params& p) {
-  return (int)(((int64_t)p.B * p.D + kThreads - 1) / kThreads);
+// Rows of all inputs on 16-byte boundaries: copies of 16 bytes.
+template <typename T>
+bool wide_ok(const ScanArgs& a) {
+  const uintptr_t all = (uintptr_t)a.gate | (uintptr_t)a.x | (uintptr_t)a.dh;
+  const int64_t st = a.p.D | a.p.gate_stride | a.p.x_stride | (a.dh ? a.p.h_stride : 0);
+  return (st * (int64_t)sizeof(T)) % 16 == 0 && (all & 15) == 0;
+}
+
+// Pairs of bf16: even width and strides, 4-byte aligned rows.
+bool pairs_ok(const ScanArgs& a) {
+  const uintptr_t all = (uintptr_t)a.gate | (uintptr_t)a.x | (uintptr_t)a.h | (uintptr_t)a.dh |
+                        (uintptr_t)a.dgate | (uintptr_t)a.dx;
+  return ((a.p.D | a.p.gate_stride | a.p.x_stride | a.p.h_stride) & 1) == 0 && (all & 3) == 0;
+}
+
+int64_t jobs_of(const spec_scan_params& p, int V) {
+  return (int64_t)p.B * ((p.D + 32 * V - 1) / (32 * V));
+}
+
+template <typename T, int V, int W>
+cudaError_t launch(ScanArgs& a, bool grad, int num_sms, cudaStream_t st) {
+  a.tiles = (a.p.D + 32 * V - 1) / (32 * V);
+  const int64_t jobs = jobs_of(a.p, V);
+  a.jobs = (int)jobs;
+  // Split a sequence over a cluster while there are not two CTAs for every SM
+  // and its steps fill more than one window.
+  int C = 1;
+  if (W > 1)
+    while (C < kMaxCluster && jobs * C < 2 * num_sms && (int64_t)C * W * kChunk < a.p.T) C *= 2;
+  a.cluster = C;
+  const int64_t grid = W == 1 ? (jobs + kSoloWarps - 1) / kSoloWarps : jobs * C;
+  if (grid > INT32_MAX) return cudaErrorInvalidValue;
+  void (*kernel)(ScanArgs) = grad ? k_scan_grad<T, V, W> : k_scan<T, V, W>;
+  const size_t smem = grad ? sizeof(GradShared<T, V, W>) : sizeof(ScanShared<T, V, W>);
+  if (smem > 48 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(32 * (W == 1 ? kSoloWarps : W));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = C;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+// A warp per job where the sequence is one piece, or where jobs alone fill the
+// GPU; else a cluster per job.
+template <typename T, int V, int W>
+cudaError_t solo_or_joined(ScanArgs& a, bool grad, int num_sms, cudaStream_t st) {
+  if (a.p.T <= kChunk || jobs_of(a.p, V) >= 16 * (int64_t)num_sms)
+    return launch<T, V, 1>(a, grad, num_sms, st);
+  return launch<T, V, W>(a, grad, num_sms, st);
+}
+
+template <typename T>
+cudaError_t dispatch(ScanArgs& a, bool grad, int num_sms, cudaStream_t st) {
+  a.wide = wide_ok<T>(a);
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+    // few channels: single ones make twice as many jobs
+    if (pairs_ok(a) && (a.p.T <= kChunk || jobs_of(a.p, 2) * kMaxCluster >= num_sms))
+      return solo_or_joined<T, 2, 8>(a, grad, num_sms, st);
+  }
+  return solo_or_joined<T, 1, 16>(a, grad, num_sms, st);
 }
 
 }  // namespace
 
 template <typename T>
 cudaError_t launch_scan(const spec_scan_params& p, const T* gate, const T* x, const float* h0,
-                        const int32_t* len, T* h, float* h_last, float* states, WsHeader* hdr, int,
-                        cudaStream_t st, int* launches) {
-  k_scan<T><<<grid_of(p), kThreads, 0, st>>>(p, gate, x, h0, len, h, h_last, states, hdr);
+                        const int32_t* len, T* h, float* h_last, float* states, WsHeader* hdr,
+                        int num_sms, cudaStream_t st, int* launches) {
+  ScanArgs a = {};
+  a.p = p;
+  a.gate = gate;
+  a.x = x;
+  a.h0 = h0;
+  a.len = len;
+  a.h = h;
+  a.h_last = h_last;
+  a.states = states;
+  a.hdr = hdr;
   *launches = 1;
-  return cudaGetLastError();
+  return dispatch<T>(a, false, num_sms, st);
 }
 
 template <typename T>
-cudaError_t launch_scan_grad(const spec_scan_params& p, const T* gate, const T* x, const float*,
+cudaError_t launch_scan_grad(const spec_scan_params& p, const T* gate, const T* x, const float* h0,
                              const int32_t* len, const float* states, const T* dh,
-                             const float* dh_last, T* dgate, T* dx, float* dh0, WsHeader* hdr, int,
-                             cudaStream_t st, int* launches) {
-  k_scan_grad<T><<<grid_of(p), kThreads, 0, st>>>(p, gate, x, len, states, dh, dh_last, dgate, dx,
-                                                  dh0, hdr);
+                             const float* dh_last, T* dgate, T* dx, float* dh0, WsHeader* hdr,
+                             int num_sms, cudaStream_t st, int* launches) {
+  ScanArgs a = {};
+  a.p = p;
+  a.gate = gate;
+  a.x = x;
+  a.h0 = h0;
+  a.len = len;
+  a.states = const_cast<float*>(states);
+  a.dh = dh;
+  a.dh_last = dh_last;
+  a.dgate = dgate;
+  a.dx = dx;
+  a.dh0 = dh0;
+  a.hdr = hdr;
   *launches = 1;
-  return cudaGetLastError();
+  return dispatch<T>(a, true, num_sms, st);
 }
 
 #define SPEC_INST(T)                                                                               \
