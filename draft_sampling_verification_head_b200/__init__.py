@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from dataclasses import dataclass
+from dataclasses import dataclass, fields
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libspecdec.so")
@@ -157,14 +157,32 @@ _DT = {"f32": SPEC_F32, "bf16": SPEC_BF16}
 
 
 class _Held:
-    """The C structure of a parameter object, made once: the objects are frozen."""
+    """What a parameter object's calls need again and again, made once: the
+    objects are frozen.  _c is the C structure, _at its address, _need the
+    workspace size and _args, by call, (name, dtype, least number of elements
+    reachable from the first one) of each tensor."""
+
+    def __getattr__(self, name):
+        if name not in ("_c", "_at", "_need", "_args"):
+            raise AttributeError(name)
+        c = self._make()
+        for k, v in (("_c", c), ("_at", ctypes.addressof(c)), ("_args", self._tensors()),
+                     ("_need", SPEC_WORKSPACE_MIN)):
+            object.__setattr__(self, k, v)
+        if isinstance(self, EmbedParams):
+            object.__setattr__(self, "_need", int(lib().spec_embed_workspace_size(self._at)))
+        return getattr(self, name)
 
     def c(self):
-        c = self.__dict__.get("_c")
-        if c is None:
-            c = self._make()
-            object.__setattr__(self, "_c", c)
-        return c
+        return self._c
+
+    def __reduce__(self):  # copies make their own C structure
+        return type(self), tuple(getattr(self, f.name) for f in fields(self))
+
+
+def _span(rows, stride, width):
+    """Elements from the first to the last of `rows` rows, `stride` (0: dense) apart."""
+    return 0 if rows <= 0 else (rows - 1) * (stride or width) + width
 
 
 @dataclass(frozen=True)
@@ -185,6 +203,13 @@ class EmbedParams(_Held):
                                1 if self.accumulate else 0, float(self.scale), 0,
                                self.table_stride, self.row_stride)
 
+    def _tensors(self):
+        table = (self.dtype, _span(self.V, self.table_stride, self.D))
+        rows = (self.row_dtype, _span(self.n, self.row_stride, self.D))
+        ids = ("ids", "i32", self.n)
+        return {"embed": (("table", *table), ids, ("rows", *rows)),
+                "embed_grad": (ids, ("drows", *rows), ("dtable", *table))}
+
 
 @dataclass(frozen=True)
 class ScanParams(_Held):
@@ -200,6 +225,19 @@ class ScanParams(_Held):
     def _make(self):
         return SpecScanParams(self.B, self.T, self.D, _DT[self.dtype], self.gate_stride,
                               self.x_stride, self.h_stride)
+
+    def _tensors(self):
+        n, e = self.B * self.T, self.B * self.D
+        gate = (self.dtype, _span(n, self.gate_stride, self.D))
+        x = (self.dtype, _span(n, self.x_stride, self.D))
+        h = (self.dtype, _span(n, self.h_stride, self.D))
+        lens = ("len", "i32", self.B)
+        states = ("states", "f32", -(-self.T // SPEC_SCAN_CHUNK) * e)
+        return {"scan": (("gate", *gate), ("x", *x), ("h0", "f32", e), lens, ("h", *h),
+                         ("h_last", "f32", e), states),
+                "scan_grad": (("gate", *gate), ("x", *x), ("h0", "f32", e), lens, states,
+                              ("dh", *h), ("dh_last", "f32", e), ("dgate", *gate), ("dx", *x),
+                              ("dh0", "f32", e))}
 
 
 @dataclass(frozen=True)
@@ -223,6 +261,16 @@ class W4Params(_Held):
                             _DT[self.scale_dtype], _DT[self.base_dtype], _DT[self.out_dtype],
                             self.x_rows, 0, self.x_stride, self.base_stride, self.out_stride)
 
+    def _tensors(self):
+        rest = (("wq", "u8", self.V * (-(-self.r // 128) * 64)),
+                ("wscale", self.scale_dtype, self.V * (self.r // max(self.group, 1))),
+                ("base", self.base_dtype, _span(self.B, self.base_stride, self.V)),
+                ("out", self.out_dtype, _span(self.B, self.out_stride, self.V)))
+        prev = ("prev", "i32", self.B)
+        return {"rows": (("x", self.dtype, _span(self.B, self.x_stride, self.r)), prev, *rest),
+                "lookup": (("x", self.dtype, _span(self.x_rows, self.x_stride, self.r)), prev,
+                           *rest)}
+
 
 @dataclass(frozen=True)
 class ProbsParams(_Held):
@@ -238,6 +286,15 @@ class ProbsParams(_Held):
     def _make(self):
         return SpecProbsParams(self.B, self.K, self.V, _DT[self.dtype], _DT[self.draft_dtype], 0,
                                self.target_stride, self.draft_stride)
+
+    def _tensors(self):
+        bk = self.B * self.K
+        return {"verify": (("target", self.dtype, _span(bk + self.B, self.target_stride, self.V)),
+                           ("draft_probs", self.draft_dtype, _span(bk, self.draft_stride, self.V)),
+                           ("draft", "i32", bk), ("u_accept", "f32", bk),
+                           ("u_draw", "f32", self.B), ("verify_len", "i32", self.B),
+                           ("out", "i32", bk + self.B), ("tau", "i32", self.B),
+                           ("p_draft", "f32", bk), ("q_draft", "f32", bk))}
 
 
 def _ptr(t):
@@ -257,10 +314,8 @@ def _check(code, what):
 
 def workspace_size(p) -> int:
     """Bytes of workspace for the calls these parameters (of any kind) belong to."""
-    if isinstance(p, EmbedParams):
-        return int(lib().spec_embed_workspace_size(ctypes.byref(p.c())))
-    if isinstance(p, (ScanParams, W4Params, ProbsParams)):
-        return SPEC_WORKSPACE_MIN
+    if isinstance(p, _Held):
+        return p._need
     return int(lib().spec_workspace_size(ctypes.byref(p.c())))
 
 
@@ -386,124 +441,106 @@ def schedule_verify_len(conf, sps):
     return kb, float(ex[0]), float(ex[1])
 
 
-def _ops(p, named, ws, stream):
-    """Raw pointers of an operator's tensors, after the checks that the C side
-    cannot make: named holds (name, tensor or None, dtype, least number of
-    elements from its first one on).  Tensors and workspace must be on the
-    current device (or the given stream's).  The elements of a tensor must be
-    reachable from its data pointer by the strides the parameters give, so a
-    strided view passes if its storage holds them."""
-    import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    dev = s.device_index
-    if dev != torch.cuda.current_device():
+_TORCH = None  # what the operators' calls use of torch, looked up once
+
+
+def _torch():
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        # the stream's handle without making a Stream object for it, where torch offers it
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda d: torch.cuda.current_stream(d).cuda_stream)
+        _TORCH = (torch.cuda.current_device, raw,
+                  {"f32": torch.float32, "bf16": torch.bfloat16, "i32": torch.int32,
+                   "u8": torch.uint8})
+    return _TORCH
+
+
+def _run(fn, p, args, tensors, ws, stream):
+    """One operator's call, after the checks that the C side cannot make.
+    Tensors, workspace and stream must belong to the current device.  The
+    elements of a tensor must be reachable from its data pointer by the strides
+    the parameters give, so a strided view passes if its storage holds them."""
+    current, raw, types = _TORCH or _torch()
+    dev = current()
+    if stream is None:
+        st = raw(dev)
+    elif stream.device_index == dev:
+        st = stream.cuda_stream
+    else:
         raise ValueError("the stream belongs to another device than the current one")
-    global _TORCH_DT
-    if _TORCH_DT is None:
-        _TORCH_DT = {"f32": torch.float32, "bf16": torch.bfloat16, "i32": torch.int32,
-                     "u8": torch.uint8}
-    out = [ctypes.byref(p.c())]
-    for name, t, dt, least in named:
+    ptr = []
+    for t, (name, dt, least) in zip(tensors, args):
         if t is None:
-            out.append(None)
+            ptr.append(None)
             continue
         if t.get_device() != dev:
             raise ValueError(f"{name} is on {t.device}, the call on cuda:{dev}")
-        if t.dtype is not _TORCH_DT[dt]:
+        if t.dtype is not types[dt]:
             raise ValueError(f"{name} is {t.dtype}, expected {dt}")
         if not t.is_contiguous() and t.stride(-1) != 1:
             raise ValueError(f"{name}: the elements of a row must be contiguous")
         if t.numel() < least and (t.untyped_storage().nbytes() // t.element_size()
                                   - t.storage_offset()) < least:
             raise ValueError(f"{name} holds {t.numel()} elements, expected {least}")
-        out.append(t.data_ptr())
-    if ws.get_device() != dev or ws.numel() * ws.element_size() < workspace_size(p):
-        raise SpecError(SPEC_ERR_WORKSPACE, "workspace too small or on another device")
-    out.append(ws.data_ptr())
-    out.append(s.cuda_stream)
-    return out
-
-
-_TORCH_DT = None
-
-
-def _span(rows, stride, width):
-    """Elements from the first to the last of `rows` rows, `stride` (0: dense) apart."""
-    return 0 if rows <= 0 else (rows - 1) * (stride or width) + width
+        ptr.append(t.data_ptr())
+    if ws.get_device() != dev or ws.nbytes < p._need:
+        raise SpecError(SPEC_ERR_WORKSPACE, f"{fn}: workspace too small or on another device")
+    code = getattr(_lib or lib(), fn)(p._at, *ptr, ws.data_ptr(), st)
+    if code != SPEC_OK:
+        raise SpecError(code, fn)
 
 
 def embed(p: EmbedParams, table, ids, rows, ws, stream=None):
     """spec_embed: rows[i] = scale * table[ids[i]] (ids int32; -1 gives zeros)."""
-    a = _ops(p, (("table", table, p.dtype, _span(p.V, p.table_stride, p.D)),
-                 ("ids", ids, "i32", p.n),
-                 ("rows", rows, p.row_dtype, _span(p.n, p.row_stride, p.D))), ws, stream)
-    _check(lib().spec_embed(*a), "spec_embed")
+    _run("spec_embed", p, p._args["embed"], (table, ids, rows), ws, stream)
 
 
 def embed_grad(p: EmbedParams, ids, drows, dtable, ws, stream=None):
     """spec_embed_grad: dtable[v] (+)= scale * sum of drows[i] with ids[i] = v."""
-    a = _ops(p, (("ids", ids, "i32", p.n),
-                 ("drows", drows, p.row_dtype, _span(p.n, p.row_stride, p.D)),
-                 ("dtable", dtable, p.dtype, _span(p.V, p.table_stride, p.D))), ws, stream)
-    _check(lib().spec_embed_grad(*a), "spec_embed_grad")
+    _run("spec_embed_grad", p, p._args["embed_grad"], (ids, drows, dtable), ws, stream)
 
 
 def gated_scan(p: ScanParams, gate, x, h0, len, h, h_last, states, ws, stream=None):
     """spec_gated_scan: h_t = f_t h_{t-1} + (1 - f_t) x_t, f = sigmoid(gate).
     h0, len, h, h_last and states may be None."""
-    n, e = p.B * p.T, p.B * p.D
-    a = _ops(p, (("gate", gate, p.dtype, _span(n, p.gate_stride, p.D)),
-                 ("x", x, p.dtype, _span(n, p.x_stride, p.D)), ("h0", h0, "f32", e),
-                 ("len", len, "i32", p.B), ("h", h, p.dtype, _span(n, p.h_stride, p.D)),
-                 ("h_last", h_last, "f32", e),
-                 ("states", states, "f32", -(-p.T // SPEC_SCAN_CHUNK) * e)), ws, stream)
-    _check(lib().spec_gated_scan(*a), "spec_gated_scan")
+    _run("spec_gated_scan", p, p._args["scan"], (gate, x, h0, len, h, h_last, states), ws, stream)
 
 
 def gated_scan_grad(p: ScanParams, gate, x, h0, len, states, dh, dh_last, dgate, dx, dh0, ws,
                     stream=None):
     """spec_gated_scan_grad: the gradients of gate, x and h0 from dh and dh_last.
     h0, len, dh_last and dh0 may be None; states as gated_scan wrote them."""
-    n, e = p.B * p.T, p.B * p.D
-    a = _ops(p, (("gate", gate, p.dtype, _span(n, p.gate_stride, p.D)),
-                 ("x", x, p.dtype, _span(n, p.x_stride, p.D)), ("h0", h0, "f32", e),
-                 ("len", len, "i32", p.B),
-                 ("states", states, "f32", -(-p.T // SPEC_SCAN_CHUNK) * e),
-                 ("dh", dh, p.dtype, _span(n, p.h_stride, p.D)), ("dh_last", dh_last, "f32", e),
-                 ("dgate", dgate, p.dtype, _span(n, p.gate_stride, p.D)),
-                 ("dx", dx, p.dtype, _span(n, p.x_stride, p.D)), ("dh0", dh0, "f32", e)), ws,
-             stream)
-    _check(lib().spec_gated_scan_grad(*a), "spec_gated_scan_grad")
+    _run("spec_gated_scan_grad", p, p._args["scan_grad"],
+         (gate, x, h0, len, states, dh, dh_last, dgate, dx, dh0), ws, stream)
 
 
 def bias_w4(p: W4Params, x, prev, wq, wscale, base, out, ws, stream=None):
     """spec_bias_w4: out = base + X . W with W in 4 bits (X[b] = x[prev[b]] or
     x[b]).  prev and base may be None."""
-    a = _ops(p, (("x", x, p.dtype, _span(p.B if prev is None else p.x_rows, p.x_stride, p.r)),
-                 ("prev", prev, "i32", p.B),
-                 ("wq", wq, "u8", p.V * (-(-p.r // 128) * 64)),
-                 ("wscale", wscale, p.scale_dtype, p.V * (p.r // p.group if p.group > 0 else 0)),
-                 ("base", base, p.base_dtype, _span(p.B, p.base_stride, p.V)),
-                 ("out", out, p.out_dtype, _span(p.B, p.out_stride, p.V))), ws, stream)
-    _check(lib().spec_bias_w4(*a), "spec_bias_w4")
+    _run("spec_bias_w4", p, p._args["rows" if prev is None else "lookup"],
+         (x, prev, wq, wscale, base, out), ws, stream)
 
 
 def w4_quantize(p: W4Params, W, stream=None):
     """spec_w4_quantize: (wq, wscale) of a factor W [r, V] (float32 or bfloat16)."""
     import torch
-    dt = "bf16" if W.dtype is torch.bfloat16 else "f32"
-    n = -(-p.r // 128) * 64
-    wq = torch.empty(p.V, n, dtype=torch.uint8, device=W.device)
+    if W.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"W is {W.dtype}, expected float32 or bfloat16")
+    if W.get_device() != torch.cuda.current_device() or not W.is_contiguous() or \
+            W.numel() < p.r * p.V:
+        raise ValueError("W must be a contiguous [r, V] tensor on the current device")
     if p.group < 1 or p.r % p.group:
         raise SpecError(SPEC_ERR_UNSUPPORTED, "spec_w4_quantize")
-    wscale = torch.empty(p.V, p.r // p.group, device=W.device,
-                         dtype=torch.bfloat16 if p.scale_dtype == "bf16" else torch.float32)
-    ws = torch.empty(SPEC_WORKSPACE_MIN, dtype=torch.uint8, device=W.device)
-    a = _ops(p, (("W", W, dt, p.r * p.V),), ws, stream)
-    if not W.is_contiguous():
-        raise ValueError("W must be contiguous")
-    _check(lib().spec_w4_quantize(a[0], a[1], _DT[dt], wq.data_ptr(), wscale.data_ptr(), a[3]),
-           "spec_w4_quantize")
+    s = stream if stream is not None else torch.cuda.current_stream()
+    with torch.cuda.stream(s):  # the outputs' memory belongs to the call's stream
+        wq = torch.empty(p.V, -(-p.r // 128) * 64, dtype=torch.uint8, device=W.device)
+        wscale = torch.empty(p.V, p.r // p.group, device=W.device,
+                             dtype=torch.bfloat16 if p.scale_dtype == "bf16" else torch.float32)
+    _check(lib().spec_w4_quantize(p._at, W.data_ptr(), SPEC_BF16 if W.dtype is torch.bfloat16
+                                  else SPEC_F32, wq.data_ptr(), wscale.data_ptr(),
+                                  s.cuda_stream), "spec_w4_quantize")
     return wq, wscale
 
 
@@ -511,14 +548,9 @@ def verify_probs(p: ProbsParams, target, draft_probs, draft, u_accept, u_draw, v
                  tau, p_draft, q_draft, ws, stream=None):
     """spec_verify_probs: verification from probabilities and given uniforms.
     verify_len, p_draft and q_draft may be None."""
-    bk = p.B * p.K
-    a = _ops(p, (("target", target, p.dtype, _span(bk + p.B, p.target_stride, p.V)),
-                 ("draft_probs", draft_probs, p.draft_dtype, _span(bk, p.draft_stride, p.V)),
-                 ("draft", draft, "i32", bk), ("u_accept", u_accept, "f32", bk),
-                 ("u_draw", u_draw, "f32", p.B), ("verify_len", verify_len, "i32", p.B),
-                 ("out", out, "i32", bk + p.B), ("tau", tau, "i32", p.B),
-                 ("p_draft", p_draft, "f32", bk), ("q_draft", q_draft, "f32", bk)), ws, stream)
-    _check(lib().spec_verify_probs(*a), "spec_verify_probs")
+    _run("spec_verify_probs", p, p._args["verify"],
+         (target, draft_probs, draft, u_accept, u_draw, verify_len, out, tau, p_draft, q_draft),
+         ws, stream)
 
 
 def last_launch_count() -> int:

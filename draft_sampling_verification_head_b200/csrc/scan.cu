@@ -210,18 +210,66 @@ SPEC_DEV void fetch(Piece<T, V>& dst, const T* src, int64_t stride, int left, in
 // recurrence.  carry holds the value before the window in every thread and
 // becomes the one after it; `before` is the one before the calling warp's
 // piece.  The slots alternate between windows, so a window needs one barrier of
-// the CTA and, in a cluster, one of the cluster.
+// the CTA.  Between the CTAs of a cluster the maps travel as asynchronous
+// stores that count their bytes on the receiver's mbarrier: a cluster barrier
+// would also wait for the outputs' stores.  A slot is free again when it is
+// written: its writer has received the window in between from the slot's owner,
+// who sent that after every warp had read the slot.
 template <int V, int W>
 struct Joiner {
   float2 piece[2][W][32 * V];
   float2 cta[2][kMaxCluster][32 * V];
+  uint64_t full[2];
 };
 template <int V>
 struct Joiner<V, 1> {};
 
+constexpr uint64_t kJoinPolls = 1ull << 22;  // about 4 s
+
 template <int V, int W>
-SPEC_DEV void join(Joiner<V, W>& sm, int par, int warp, int rank, int cluster, Vec<V> a, Vec<V> c,
-                   Vec<V>& carry, Vec<V>& before) {
+SPEC_DEV void join_init(Joiner<V, W>& sm, int cluster) {
+  if constexpr (W > 1) {
+    if (cluster == 1) return;
+    if (threadIdx.x == 0) {
+      mbar_init(&sm.full[0], 1);
+      mbar_init(&sm.full[1], 1);
+      fence_mbar_init();
+    }
+    cg::this_cluster().sync();  // every CTA runs, its barriers ready, before another writes to it
+  }
+}
+
+SPEC_DEV uint32_t at_rank(uint32_t addr, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+SPEC_DEV void send(uint32_t to, float2 v, uint32_t bar) {
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(
+          to),
+      "f"(v.x), "f"(v.y), "r"(bar)
+      : "memory");
+}
+SPEC_DEV bool cluster_wait(uint64_t* bar, uint32_t parity) {
+  for (uint64_t it = 0; it < kJoinPolls; ++it) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(1000u)
+        : "memory");
+    if (ok) return true;
+  }
+  return false;
+}
+
+template <int V, int W>
+SPEC_DEV void join(Joiner<V, W>& sm, int win, int warp, int rank, int cluster, Vec<V> a, Vec<V> c,
+                   Vec<V>& carry, Vec<V>& before, WsHeader* hdr) {
+  const int par = win & 1;
   if constexpr (W == 1) {
     before = carry;
     carry = fma(a, carry, c);
@@ -246,10 +294,9 @@ SPEC_DEV void join(Joiner<V, W>& sm, int par, int warp, int rank, int cluster, V
         tc = fmaf(m.x, tc, m.y);
       }
       if (cluster > 1) {
-        if (warp < cluster) {  // the warps hand the CTA's map to one CTA each
-          Joiner<V, W>* far = cg::this_cluster().map_shared_rank(&sm, warp);
-          far->cta[par][rank][v * 32 + lane] = make_float2(ta, tc);
-        }
+        if (warp < cluster)  // the warps hand the CTA's map to one CTA each
+          send(at_rank(smem_u32(&sm.cta[par][rank][v * 32 + lane]), warp), make_float2(ta, tc),
+               at_rank(smem_u32(&sm.full[par]), warp));
         out_b[v] = pa;
         out_c[v] = pc;
       } else {
@@ -258,7 +305,10 @@ SPEC_DEV void join(Joiner<V, W>& sm, int par, int warp, int rank, int cluster, V
       }
     }
     if (cluster > 1) {
-      cg::this_cluster().sync();
+      if (threadIdx.x == 0)
+        mbar_arrive_expect_tx(&sm.full[par], (uint32_t)(cluster * 32 * V * sizeof(float2)));
+      if (!cluster_wait(&sm.full[par], (win >> 1) & 1) && threadIdx.x == 0)
+        report_error(hdr, SPEC_ERR_TIMEOUT, SITE_MBAR_FULL, rank, win);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         float s = carry.get(v), mine = s;
@@ -334,7 +384,7 @@ __global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), W == 16 ? 1 : 
     cp_async_commit();
   };
   request(t0);
-  if (C > 1) cg::this_cluster().sync();  // every CTA runs before another writes to it
+  join_init<V, W>(sm.joiner, C);
   const int nwin = (Tn + window - 1) / window;
   for (int win = 0; win < nwin; ++win, t0 += window) {
     Vec<V> f[kChunk], z[kChunk], ma = Vec<V>::all(1.f), mc = Vec<V>::all(0.f);
@@ -362,16 +412,24 @@ __global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), W == 16 ? 1 : 
     __syncwarp();
     request(t0 + window);
     Vec<V> s;
-    join<V, W>(sm.joiner, win & 1, warp, rank, C, ma, mc, carry, s);
+    join<V, W>(sm.joiner, win, warp, rank, C, ma, mc, carry, s, a.hdr);
     if (on && a.states && t0 < Tn)
       state_store<V>(a.states + ((int64_t)b * nch + t0 / kChunk) * D + c, s);
     if (on && a.h && left > 0) {
       T* h = hp + (int64_t)t0 * a.p.h_stride;
+      const int hs = (int)a.p.h_stride;
+      if (left >= kChunk) {
 #pragma unroll
-      for (int k = 0; k < kChunk; ++k) {
-        s = fma(f[k], s, z[k]);
-        if (k < left) raw_store<T, V>(h, s);
-        h += a.p.h_stride;
+        for (int k = 0; k < kChunk; ++k) {
+          s = fma(f[k], s, z[k]);
+          raw_store<T, V>(h + (int64_t)k * hs, s);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < kChunk; ++k) {
+          s = fma(f[k], s, z[k]);
+          if (k < left) raw_store<T, V>(h + (int64_t)k * hs, s);
+        }
       }
     }
     __syncwarp();
@@ -427,7 +485,7 @@ __global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), W == 16 ? 1 : 
     s0 = state_load<V>(a.states + ((int64_t)b * nch + q) * D + c, on && q >= 0);
   };
   request(ch, 0);
-  if (C > 1) cg::this_cluster().sync();  // every CTA runs before another writes to it
+  join_init<V, W>(sm.joiner, C);
   const int nwin = (nch + window - 1) / window;
   for (int win = 0; win < nwin; ++win, ch -= window) {
     const int t0 = ch * kChunk, left = ch < 0 ? 0 : n - t0, par = win & 1;
@@ -458,24 +516,31 @@ __global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), W == 16 ? 1 : 
     }
     __syncwarp();
     request(ch - window, par ^ 1);
-    join<V, W>(sm.joiner, par, warp, rank, C, ma, mc, carry, s);
+    join<V, W>(sm.joiner, win, warp, rank, C, ma, mc, carry, s, a.hdr);
     if (on && ch >= 0) {
-      const int rows = min(kChunk, Tn - t0);
-      T* dg = dgp + (int64_t)(t0 + kChunk - 1) * a.p.gate_stride;
-      T* dx = dxp + (int64_t)(t0 + kChunk - 1) * a.p.x_stride;
+      T* dg = dgp + (int64_t)t0 * a.p.gate_stride;
+      T* dx = dxp + (int64_t)t0 * a.p.x_stride;
+      const int gs = (int)a.p.gate_stride, xs = (int)a.p.x_stride;
+      if (left >= kChunk) {
 #pragma unroll
-      for (int k = kChunk - 1; k >= 0; --k) {
-        const Vec<V> delta = s + raw_value<T, V>(sm.dh[par][wid].at[k][lane]);
-        if (k < left) {
-          raw_store<T, V>(dg, delta * w[k]);
-          raw_store<T, V>(dx, delta * i[k]);
-        } else if (k < rows) {
-          raw_store<T, V>(dg, Vec<V>::all(0.f));
-          raw_store<T, V>(dx, Vec<V>::all(0.f));
+        for (int k = kChunk - 1; k >= 0; --k) {
+          const Vec<V> delta = s + raw_value<T, V>(sm.dh[par][wid].at[k][lane]);
+          raw_store<T, V>(dg + (int64_t)k * gs, delta * w[k]);
+          raw_store<T, V>(dx + (int64_t)k * xs, delta * i[k]);
+          s = delta * f[k];
         }
-        s = delta * f[k];
-        dg -= a.p.gate_stride;
-        dx -= a.p.x_stride;
+      } else {
+        const int rows = min(kChunk, Tn - t0);
+#pragma unroll
+        for (int k = kChunk - 1; k >= 0; --k) {
+          const Vec<V> delta = s + raw_value<T, V>(sm.dh[par][wid].at[k][lane]);
+          const Vec<V> zero = Vec<V>::all(0.f);
+          if (k < rows) {
+            raw_store<T, V>(dg + (int64_t)k * gs, k < left ? delta * w[k] : zero);
+            raw_store<T, V>(dx + (int64_t)k * xs, k < left ? delta * i[k] : zero);
+          }
+          s = delta * f[k];
+        }
       }
     }
     __syncwarp();
