@@ -44,6 +44,7 @@ _SIGS = {
     "spec_embed_workspace_size": (ctypes.c_size_t, [_P]),
     "spec_embed": (ctypes.c_int, [_P] * 6),
     "spec_embed_grad": (ctypes.c_int, [_P] * 6),
+    "spec_scan_workspace_size": (ctypes.c_size_t, [_P]),
     "spec_gated_scan": (ctypes.c_int, [_P] * 10),
     "spec_gated_scan_grad": (ctypes.c_int, [_P] * 13),
     "spec_bias_w4": (ctypes.c_int, [_P] * 9),
@@ -171,6 +172,8 @@ class _Held:
             object.__setattr__(self, k, v)
         if isinstance(self, EmbedParams):
             object.__setattr__(self, "_need", int(lib().spec_embed_workspace_size(self._at)))
+        elif isinstance(self, ScanParams):
+            object.__setattr__(self, "_need", int(lib().spec_scan_workspace_size(self._at)))
         return getattr(self, name)
 
     def c(self):

@@ -158,6 +158,14 @@ spec_status spec_embed_grad(const spec_embed_params* p, const int32_t* ids, cons
   return launched(e, launches);
 }
 
+size_t spec_scan_workspace_size(const spec_scan_params* p) {
+  spec_scan_params d;
+  if (check_scan(p, &d) != SPEC_OK) return 0;
+  const int sms = num_sms();
+  if (sms <= 0) return 0;
+  return (sizeof(WsHeader) + scan_ws_bytes(d, sms) + 255) & ~size_t(255);
+}
+
 spec_status spec_gated_scan(const spec_scan_params* p, const void* gate, const void* x,
                             const float* h0, const int32_t* len, void* h, float* h_last,
                             float* states, void* ws, spec_stream_t stream) {
@@ -178,10 +186,10 @@ spec_status spec_gated_scan(const spec_scan_params* p, const void* gate, const v
   const cudaError_t e =
       d.dtype == SPEC_BF16
           ? launch_scan(d, (const __nv_bfloat16*)gate, (const __nv_bfloat16*)x, h0, len,
-                        (__nv_bfloat16*)h, h_last, states, header_of(ws), sms,
+                        (__nv_bfloat16*)h, h_last, states, body_of(ws), header_of(ws), sms,
                         (cudaStream_t)stream, &launches)
           : launch_scan(d, (const float*)gate, (const float*)x, h0, len, (float*)h, h_last, states,
-                        header_of(ws), sms, (cudaStream_t)stream, &launches);
+                        body_of(ws), header_of(ws), sms, (cudaStream_t)stream, &launches);
   return launched(e, launches);
 }
 
@@ -207,11 +215,11 @@ spec_status spec_gated_scan_grad(const spec_scan_params* p, const void* gate, co
       d.dtype == SPEC_BF16
           ? launch_scan_grad(d, (const __nv_bfloat16*)gate, (const __nv_bfloat16*)x, h0, len,
                              states, (const __nv_bfloat16*)dh, dh_last, (__nv_bfloat16*)dgate,
-                             (__nv_bfloat16*)dx, dh0, header_of(ws), sms, (cudaStream_t)stream,
+                             (__nv_bfloat16*)dx, dh0, body_of(ws), header_of(ws), sms, (cudaStream_t)stream,
                              &launches)
           : launch_scan_grad(d, (const float*)gate, (const float*)x, h0, len, states,
                              (const float*)dh, dh_last, (float*)dgate, (float*)dx, dh0,
-                             header_of(ws), sms, (cudaStream_t)stream, &launches);
+                             body_of(ws), header_of(ws), sms, (cudaStream_t)stream, &launches);
   return launched(e, launches);
 }
 

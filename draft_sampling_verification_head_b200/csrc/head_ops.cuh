@@ -32,15 +32,16 @@ cudaError_t launch_embed_grad(const spec_embed_params& p, const int32_t* ids, co
                               cudaStream_t st, int* launches);
 
 // ---- Gated linear recurrence and its gradient -------------------------------------
+size_t scan_ws_bytes(const spec_scan_params& p, int num_sms);
 template <typename T>
 cudaError_t launch_scan(const spec_scan_params& p, const T* gate, const T* x, const float* h0,
-                        const int32_t* len, T* h, float* h_last, float* states, WsHeader* hdr,
-                        int num_sms, cudaStream_t st, int* launches);
+                        const int32_t* len, T* h, float* h_last, float* states, uint8_t* body,
+                        WsHeader* hdr, int num_sms, cudaStream_t st, int* launches);
 template <typename T>
 cudaError_t launch_scan_grad(const spec_scan_params& p, const T* gate, const T* x, const float* h0,
                              const int32_t* len, const float* states, const T* dh,
-                             const float* dh_last, T* dgate, T* dx, float* dh0, WsHeader* hdr,
-                             int num_sms, cudaStream_t st, int* launches);
+                             const float* dh_last, T* dgate, T* dx, float* dh0, uint8_t* body,
+                             WsHeader* hdr, int num_sms, cudaStream_t st, int* launches);
 
 // ---- Vocabulary product with 4-bit weights ------------------------------------------
 template <typename T>

@@ -12,6 +12,7 @@
 // the joins are taken in a fixed order.
 #include <cooperative_groups.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "head_ops.cuh"
@@ -24,6 +25,8 @@ namespace {
 constexpr int kChunk = SPEC_SCAN_CHUNK;  // steps per piece
 constexpr int kMaxCluster = 8;           // CTAs per cluster (portable limit)
 constexpr int kSoloWarps = 8;            // warps per CTA where each has a job of its own
+constexpr int kSplitSteps = 1024;        // shortest sequence whose steps are split
+constexpr int kMinSegment = 64;          // shortest segment
 
 SPEC_DEV int len_of(const int32_t* len, int b, int T, WsHeader* hdr, bool say) {
   if (!len) return T;
@@ -164,8 +167,28 @@ struct ScanArgs {
   int tiles;    // channel tiles per sequence
   int cluster;  // CTAs per cluster
   int wide;     // rows lie on 16-byte boundaries
-  int jobs;     // sequences x tiles
+  int jobs;     // sequences x tiles (x segments)
+  int nseg;     // segments per sequence, where a warp has one of its own
+  int seg;      // steps per segment, a multiple of kChunk
+  float2* maps;   // [B][nseg][D] a segment's map
+  float* starts;  // [B][nseg][D] the value a segment starts from
 };
+
+// Where a job of a warp of its own lies: a sequence, a tile of channels, and a
+// segment of the steps (all of them where nothing is split).
+struct Place {
+  int b, ct, seg, t0, t1;
+};
+SPEC_DEV Place place_of(const ScanArgs& a, int job, int width) {
+  Place p;
+  p.seg = job % a.nseg;
+  job /= a.nseg;
+  p.b = job / a.tiles;
+  p.ct = (job % a.tiles) * width;
+  p.t0 = p.seg * a.seg;
+  p.t1 = min(p.t0 + a.seg, a.p.T);
+  return p;
+}
 
 // One piece of one input in shared memory, written by 16-byte asynchronous
 // copies where rows allow (zero-filled behind the end), else by plain loads.
@@ -363,21 +386,25 @@ __global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), W == 16 ? 1 : 
   const int C = W == 1 ? 1 : a.cluster, rank = blockIdx.x % C, warp = W == 1 ? 0 : wid;
   const int job = W == 1 ? blockIdx.x * kSoloWarps + wid : blockIdx.x / C;
   if (job >= a.jobs) return;  // W = 1 only: whole warps, and no barrier follows
-  const int b = job / a.tiles, ct = (job % a.tiles) * (32 * V), c = ct + lane * V;
+  const Place at = place_of(a, job, 32 * V);
+  const int b = at.b, ct = at.ct, c = ct + lane * V;
   const int D = a.p.D, Tn = a.p.T;
   const bool on = c < D;  // pairs are only taken where D is even
-  const int n = len_of(a.len, b, Tn, a.hdr, ct == 0 && rank == 0 && warp == 0 && lane == 0);
+  const int n = len_of(a.len, b, Tn, a.hdr,
+                       ct == 0 && at.seg == 0 && rank == 0 && warp == 0 && lane == 0);
   const int64_t row0 = (int64_t)b * Tn;
   const T* gp = (const T*)a.gate + row0 * a.p.gate_stride + ct;
   const T* xp = (const T*)a.x + row0 * a.p.x_stride + ct;
   T* hp = (T*)a.h + row0 * a.p.h_stride + c;
   const int nch = (Tn + kChunk - 1) / kChunk;
-  Vec<V> carry = state_load<V>(a.h0 + (int64_t)b * D + c, a.h0 && on);
+  Vec<V> carry = a.nseg > 1
+                     ? state_load<V>(a.starts + ((int64_t)b * a.nseg + at.seg) * D + c, on)
+                     : state_load<V>(a.h0 + (int64_t)b * D + c, a.h0 && on);
 
   const int window = C * W * kChunk;
-  int t0 = (rank * W + warp) * kChunk;
+  int t0 = at.t0 + (rank * W + warp) * kChunk;
   auto request = [&](int t) {
-    if (t < n) {
+    if (t < min(n, at.t1)) {
       fetch(sm.gate[wid], gp + (int64_t)t * a.p.gate_stride, a.p.gate_stride, n - t, D - ct, a.wide);
       fetch(sm.x[wid], xp + (int64_t)t * a.p.x_stride, a.p.x_stride, n - t, D - ct, a.wide);
     }
@@ -385,7 +412,7 @@ __global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), W == 16 ? 1 : 
   };
   request(t0);
   join_init<V, W>(sm.joiner, C);
-  const int nwin = (Tn + window - 1) / window;
+  const int nwin = (at.t1 - at.t0 + window - 1) / window;
   for (int win = 0; win < nwin; ++win, t0 += window) {
     Vec<V> f[kChunk], z[kChunk], ma = Vec<V>::all(1.f), mc = Vec<V>::all(0.f);
     cp_async_wait<0>();
@@ -434,7 +461,7 @@ __global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), W == 16 ? 1 : 
     }
     __syncwarp();
   }
-  if (a.h_last && rank == 0 && warp == 0 && on)
+  if (a.h_last && at.seg == a.nseg - 1 && rank == 0 && warp == 0 && on)
     state_store<V>(a.h_last + (int64_t)b * D + c, carry);
 }
 
@@ -458,10 +485,12 @@ __global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), W == 16 ? 1 : 
   const int C = W == 1 ? 1 : a.cluster, rank = blockIdx.x % C, warp = W == 1 ? 0 : wid;
   const int job = W == 1 ? blockIdx.x * kSoloWarps + wid : blockIdx.x / C;
   if (job >= a.jobs) return;  // W = 1 only: whole warps, and no barrier follows
-  const int b = job / a.tiles, ct = (job % a.tiles) * (32 * V), c = ct + lane * V;
+  const Place at = place_of(a, job, 32 * V);
+  const int b = at.b, ct = at.ct, c = ct + lane * V;
   const int D = a.p.D, Tn = a.p.T;
   const bool on = c < D;
-  const int n = len_of(a.len, b, Tn, a.hdr, ct == 0 && rank == 0 && warp == 0 && lane == 0);
+  const int n = len_of(a.len, b, Tn, a.hdr,
+                       ct == 0 && at.seg == 0 && rank == 0 && warp == 0 && lane == 0);
   const int64_t row0 = (int64_t)b * Tn;
   const T* gp = (const T*)a.gate + row0 * a.p.gate_stride + ct;
   const T* xp = (const T*)a.x + row0 * a.p.x_stride + ct;
@@ -469,26 +498,29 @@ __global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), W == 16 ? 1 : 
   T* dgp = (T*)a.dgate + row0 * a.p.gate_stride + c;
   T* dxp = (T*)a.dx + row0 * a.p.x_stride + c;
   const int nch = (Tn + kChunk - 1) / kChunk;
-  Vec<V> carry = state_load<V>(a.dh_last + (int64_t)b * D + c, a.dh_last && on);
+  Vec<V> carry = a.nseg > 1
+                     ? state_load<V>(a.starts + ((int64_t)b * a.nseg + at.seg) * D + c, on)
+                     : state_load<V>(a.dh_last + (int64_t)b * D + c, a.dh_last && on);
 
   const int window = C * W;  // in pieces
-  int ch = nch - 1 - (rank * W + warp);
+  const int ch0 = at.t0 / kChunk, ch1 = (at.t1 + kChunk - 1) / kChunk;
+  int ch = ch1 - 1 - (rank * W + warp);
   Vec<V> s0;
   auto request = [&](int q, int par) {
     const int t = q * kChunk;
-    if (q >= 0 && t < n) {
+    if (q >= ch0 && t < n) {
       fetch(sm.gate[wid], gp + (int64_t)t * a.p.gate_stride, a.p.gate_stride, n - t, D - ct, a.wide);
       fetch(sm.x[wid], xp + (int64_t)t * a.p.x_stride, a.p.x_stride, n - t, D - ct, a.wide);
       fetch(sm.dh[par][wid], dp + (int64_t)t * a.p.h_stride, a.p.h_stride, n - t, D - ct, a.wide);
     }
     cp_async_commit();
-    s0 = state_load<V>(a.states + ((int64_t)b * nch + q) * D + c, on && q >= 0);
+    s0 = state_load<V>(a.states + ((int64_t)b * nch + q) * D + c, on && q >= ch0);
   };
   request(ch, 0);
   join_init<V, W>(sm.joiner, C);
-  const int nwin = (nch + window - 1) / window;
+  const int nwin = (ch1 - ch0 + window - 1) / window;
   for (int win = 0; win < nwin; ++win, ch -= window) {
-    const int t0 = ch * kChunk, left = ch < 0 ? 0 : n - t0, par = win & 1;
+    const int t0 = ch * kChunk, left = ch < ch0 ? 0 : n - t0, par = win & 1;
     Vec<V> f[kChunk], i[kChunk], w[kChunk], ma = Vec<V>::all(1.f), mc = Vec<V>::all(0.f);
     cp_async_wait<0>();
     __syncwarp();
@@ -517,7 +549,7 @@ __global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), W == 16 ? 1 : 
     __syncwarp();
     request(ch - window, par ^ 1);
     join<V, W>(sm.joiner, win, warp, rank, C, ma, mc, carry, s, a.hdr);
-    if (on && ch >= 0) {
+    if (on && ch >= ch0) {
       T* dg = dgp + (int64_t)t0 * a.p.gate_stride;
       T* dx = dxp + (int64_t)t0 * a.p.x_stride;
       const int gs = (int)a.p.gate_stride, xs = (int)a.p.x_stride;
@@ -545,8 +577,109 @@ __global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), W == 16 ? 1 : 
     }
     __syncwarp();
   }
-  if (a.dh0 && rank == 0 && warp == 0 && on)
+  if (a.dh0 && at.seg == 0 && rank == 0 && warp == 0 && on)
     state_store<V>(a.dh0 + (int64_t)b * D + c, carry);
+}
+
+// ----------------------------------------------------------------------------
+// Long sequences of few channels: even a cluster per job leaves most of the GPU
+// idle, so the steps are split into segments, a warp each.  One pass reduces
+// every segment to its map, a small kernel joins the maps into the values that
+// the segments start from, and the kernels above run with a warp per segment.
+// The inputs of the recurrence are read twice, the second time mostly from L2.
+// ----------------------------------------------------------------------------
+constexpr int kMapWarps = 4;
+
+template <typename T, int V, bool kGrad>
+__global__ void __launch_bounds__(32 * kMapWarps) k_scan_maps(ScanArgs a) {
+  __shared__ Piece<T, V> gate[kMapWarps][2], other[kMapWarps][2];
+  const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int job = blockIdx.x * kMapWarps + wid;
+  if (job >= a.jobs) return;
+  const Place at = place_of(a, job, 32 * V);
+  const int b = at.b, ct = at.ct, c = ct + lane * V, D = a.p.D;
+  const int n = len_of(a.len, b, a.p.T, a.hdr, false);
+  const int64_t row0 = (int64_t)b * a.p.T;
+  const int64_t stride = kGrad ? a.p.h_stride : a.p.x_stride;
+  const T* gp = (const T*)a.gate + row0 * a.p.gate_stride + ct;
+  const T* op = (const T*)(kGrad ? a.dh : a.x) + row0 * stride + ct;
+  const int ch0 = at.t0 / kChunk, ch1 = (at.t1 + kChunk - 1) / kChunk;
+  // the pieces in the order of the recurrence
+  auto piece = [&](int q) { return kGrad ? ch1 - 1 - q : ch0 + q; };
+  auto request = [&](int q) {
+    const int t = piece(q) * kChunk;
+    if (q < ch1 - ch0 && t < n) {
+      fetch(gate[wid][q & 1], gp + (int64_t)t * a.p.gate_stride, a.p.gate_stride, n - t, D - ct, a.wide);
+      fetch(other[wid][q & 1], op + (int64_t)t * stride, stride, n - t, D - ct, a.wide);
+    }
+    cp_async_commit();
+  };
+  Vec<V> ma = Vec<V>::all(1.f), mc = Vec<V>::all(0.f);
+  request(0);
+  for (int q = 0; q < ch1 - ch0; ++q) {
+    request(q + 1);
+    cp_async_wait<1>();
+    __syncwarp();
+    const int left = n - piece(q) * kChunk;
+    auto step = [&](int k) {
+      Vec<V> f, i;
+      gate_of<T, V>(gate[wid][q & 1].at[k][lane], f, i);
+      const Vec<V> o = raw_value<T, V>(other[wid][q & 1].at[k][lane]);
+      ma = ma * f;
+      if constexpr (kGrad)
+        mc = f * (mc + o);
+      else
+        mc = fma(f, mc, i * o);
+    };
+    if (left >= kChunk) {
+#pragma unroll
+      for (int k = 0; k < kChunk; ++k) step(kGrad ? kChunk - 1 - k : k);
+    } else {
+      for (int k = 0; k < left; ++k) step(kGrad ? left - 1 - k : k);
+    }
+    __syncwarp();
+  }
+  if (c < D) {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      a.maps[((int64_t)b * a.nseg + at.seg) * D + c + v] = make_float2(ma.get(v), mc.get(v));
+  }
+}
+
+constexpr int kJoinWarps = 16;
+
+// One CTA per sequence and 32 channels; a warp takes a run of segments.
+__global__ void __launch_bounds__(32 * kJoinWarps) k_scan_starts(ScanArgs a, bool grad) {
+  __shared__ float2 part[kJoinWarps][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int D = a.p.D, tiles = (D + 31) / 32, b = blockIdx.x / tiles;
+  const int c = (blockIdx.x % tiles) * 32 + lane;
+  const bool on = c < D;
+  const int per = (a.nseg + kJoinWarps - 1) / kJoinWarps;
+  const int q0 = min(warp * per, a.nseg), q1 = min(q0 + per, a.nseg);
+  const int64_t row = (int64_t)b * a.nseg;
+  // the segments in the order of the recurrence
+  auto at = [&](int q) { return (row + (grad ? a.nseg - 1 - q : q)) * D + c; };
+  float ma = 1.f, mc = 0.f;
+#pragma unroll 8
+  for (int q = q0; q < q1; ++q) {
+    const float2 m = on ? a.maps[at(q)] : make_float2(1.f, 0.f);
+    ma *= m.x;
+    mc = fmaf(m.x, mc, m.y);
+  }
+  part[warp][lane] = make_float2(ma, mc);
+  __syncthreads();
+  const float* first = grad ? a.dh_last : a.h0;
+  float s = first && on ? first[(int64_t)b * D + c] : 0.f;
+  for (int w = 0; w < warp; ++w) s = fmaf(part[w][lane].x, s, part[w][lane].y);
+#pragma unroll 8
+  for (int q = q0; q < q1; ++q) {
+    if (on) {
+      const float2 m = a.maps[at(q)];
+      a.starts[at(q)] = s;
+      s = fmaf(m.x, s, m.y);
+    }
+  }
 }
 
 // Rows of all inputs on 16-byte boundaries: copies of 16 bytes.
@@ -568,10 +701,20 @@ int64_t jobs_of(const spec_scan_params& p, int V) {
   return (int64_t)p.B * ((p.D + 32 * V - 1) / (32 * V));
 }
 
+// Steps per segment where the steps are split, 0 where they are not.  Split
+// when clusters of every job would still leave SMs without a CTA and the steps
+// fill several of their windows; segments then give every SM about 16 warps.
+int segment_steps(const spec_scan_params& p, int64_t jobs, int num_sms) {
+  if (jobs * kMaxCluster >= num_sms || p.T < kSplitSteps) return 0;
+  const int64_t segs = (16 * (int64_t)num_sms + jobs - 1) / jobs;
+  const int64_t steps = (p.T + segs - 1) / segs;
+  return (int)std::max<int64_t>((steps + kChunk - 1) / kChunk * kChunk, kMinSegment);
+}
+
 template <typename T, int V, int W>
 cudaError_t launch(ScanArgs& a, bool grad, int num_sms, cudaStream_t st) {
+  const int64_t jobs = jobs_of(a.p, V) * a.nseg;
   a.tiles = (a.p.D + 32 * V - 1) / (32 * V);
-  const int64_t jobs = jobs_of(a.p, V);
   a.jobs = (int)jobs;
   // Split a sequence over a cluster while there are not two CTAs for every SM
   // and its steps fill more than one window.
@@ -602,32 +745,64 @@ cudaError_t launch(ScanArgs& a, bool grad, int num_sms, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-// A warp per job where the sequence is one piece, or where jobs alone fill the
-// GPU; else a cluster per job.
 template <typename T, int V, int W>
-cudaError_t solo_or_joined(ScanArgs& a, bool grad, int num_sms, cudaStream_t st) {
+cudaError_t by_shape(ScanArgs& a, bool grad, int num_sms, uint8_t* body, cudaStream_t st,
+                     int* launches) {
+  a.nseg = 1;
+  a.seg = a.p.T;
+  *launches = 1;
+  // a warp per job where the sequence is one piece, or where jobs fill the GPU
   if (a.p.T <= kChunk || jobs_of(a.p, V) >= 16 * (int64_t)num_sms)
     return launch<T, V, 1>(a, grad, num_sms, st);
-  return launch<T, V, W>(a, grad, num_sms, st);
+  a.seg = segment_steps(a.p, jobs_of(a.p, V), num_sms);
+  if (a.seg == 0) {
+    a.seg = a.p.T;
+    return launch<T, V, W>(a, grad, num_sms, st);
+  }
+  a.nseg = (a.p.T + a.seg - 1) / a.seg;
+  a.tiles = (a.p.D + 32 * V - 1) / (32 * V);
+  a.jobs = (int)(jobs_of(a.p, V) * a.nseg);
+  a.maps = reinterpret_cast<float2*>(body);
+  a.starts = reinterpret_cast<float*>(a.maps + (size_t)a.p.B * a.nseg * a.p.D);
+  const int grid = (a.jobs + kMapWarps - 1) / kMapWarps;
+  if (grad)
+    k_scan_maps<T, V, true><<<grid, 32 * kMapWarps, 0, st>>>(a);
+  else
+    k_scan_maps<T, V, false><<<grid, 32 * kMapWarps, 0, st>>>(a);
+  k_scan_starts<<<(int)jobs_of(a.p, 1), 32 * kJoinWarps, 0, st>>>(a, grad);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  *launches = 3;
+  return launch<T, V, 1>(a, grad, num_sms, st);
 }
 
 template <typename T>
-cudaError_t dispatch(ScanArgs& a, bool grad, int num_sms, cudaStream_t st) {
+cudaError_t dispatch(ScanArgs& a, bool grad, int num_sms, uint8_t* body, cudaStream_t st,
+                     int* launches) {
   a.wide = wide_ok<T>(a);
   if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-    // few channels: single ones make twice as many jobs
-    if (pairs_ok(a) && (a.p.T <= kChunk || jobs_of(a.p, 2) * kMaxCluster >= num_sms))
-      return solo_or_joined<T, 2, 8>(a, grad, num_sms, st);
+    if (pairs_ok(a)) return by_shape<T, 2, 8>(a, grad, num_sms, body, st, launches);
   }
-  return solo_or_joined<T, 1, 16>(a, grad, num_sms, st);
+  return by_shape<T, 1, 16>(a, grad, num_sms, body, st, launches);
 }
 
 }  // namespace
 
+size_t scan_ws_bytes(const spec_scan_params& p, int num_sms) {
+  size_t need = 0;
+  for (int V = 1; V <= (p.dtype == SPEC_BF16 ? 2 : 1); ++V) {  // whichever alignment allows
+    const int seg = segment_steps(p, jobs_of(p, V), num_sms);
+    if (seg == 0) continue;
+    const size_t nseg = (p.T + seg - 1) / seg;
+    need = std::max(need, (sizeof(float2) + sizeof(float)) * (size_t)p.B * nseg * p.D);
+  }
+  return need;
+}
+
 template <typename T>
 cudaError_t launch_scan(const spec_scan_params& p, const T* gate, const T* x, const float* h0,
-                        const int32_t* len, T* h, float* h_last, float* states, WsHeader* hdr,
-                        int num_sms, cudaStream_t st, int* launches) {
+                        const int32_t* len, T* h, float* h_last, float* states, uint8_t* body,
+                        WsHeader* hdr, int num_sms, cudaStream_t st, int* launches) {
   ScanArgs a = {};
   a.p = p;
   a.gate = gate;
@@ -638,15 +813,14 @@ cudaError_t launch_scan(const spec_scan_params& p, const T* gate, const T* x, co
   a.h_last = h_last;
   a.states = states;
   a.hdr = hdr;
-  *launches = 1;
-  return dispatch<T>(a, false, num_sms, st);
+  return dispatch<T>(a, false, num_sms, body, st, launches);
 }
 
 template <typename T>
 cudaError_t launch_scan_grad(const spec_scan_params& p, const T* gate, const T* x, const float* h0,
                              const int32_t* len, const float* states, const T* dh,
-                             const float* dh_last, T* dgate, T* dx, float* dh0, WsHeader* hdr,
-                             int num_sms, cudaStream_t st, int* launches) {
+                             const float* dh_last, T* dgate, T* dx, float* dh0, uint8_t* body,
+                             WsHeader* hdr, int num_sms, cudaStream_t st, int* launches) {
   ScanArgs a = {};
   a.p = p;
   a.gate = gate;
@@ -660,17 +834,16 @@ cudaError_t launch_scan_grad(const spec_scan_params& p, const T* gate, const T* 
   a.dx = dx;
   a.dh0 = dh0;
   a.hdr = hdr;
-  *launches = 1;
-  return dispatch<T>(a, true, num_sms, st);
+  return dispatch<T>(a, true, num_sms, body, st, launches);
 }
 
 #define SPEC_INST(T)                                                                               \
   template cudaError_t launch_scan<T>(const spec_scan_params&, const T*, const T*, const float*,   \
-                                      const int32_t*, T*, float*, float*, WsHeader*, int,          \
+                                      const int32_t*, T*, float*, float*, uint8_t*, WsHeader*, int, \
                                       cudaStream_t, int*);                                         \
   template cudaError_t launch_scan_grad<T>(const spec_scan_params&, const T*, const T*,            \
                                            const float*, const int32_t*, const float*, const T*,   \
-                                           const float*, T*, T*, float*, WsHeader*, int,           \
+                                           const float*, T*, T*, float*, uint8_t*, WsHeader*, int, \
                                            cudaStream_t, int*);
 SPEC_INST(float)
 SPEC_INST(__nv_bfloat16)

@@ -299,13 +299,14 @@ spec_status spec_l2_persist(const void *ptr, size_t bytes, spec_stream_t stream)
  * current device, rows contiguous, any element alignment (16-byte aligned
  * pointers and row strides run faster); strides are in elements, 0 = dense.
  * Outputs may not overlap inputs unless a comment says so.  `workspace` holds
- * at least SPEC_WORKSPACE_MIN bytes (spec_embed_grad: what
- * spec_embed_workspace_size returns), zeroed once by spec_workspace_init; errors found
- * on the device go there and are read by spec_sync_status.  spec_embed_grad
- * writes all over its workspace, so that one serves no other call; the others
- * touch only the status and may share any workspace.  All calls can be
- * captured into a CUDA graph.  No call waits for another CTA's progress, sums
- * are taken in a fixed order, and equal inputs give equal bits.
+ * at least SPEC_WORKSPACE_MIN bytes (spec_embed_grad and the recurrence: what
+ * spec_embed_workspace_size and spec_scan_workspace_size return), zeroed once
+ * by spec_workspace_init; errors found on the device go there and are read by
+ * spec_sync_status.  spec_embed_grad and the recurrence also keep scratch in
+ * it, which calls of one stream may share among themselves, but not with the
+ * calls above; the others touch only the status and may share any workspace.
+ * All calls can be captured into a CUDA graph.  Sums are taken in a fixed
+ * order, and equal inputs give equal bits.
  * ------------------------------------------------------------------------- */
 #define SPEC_WORKSPACE_MIN 256
 
@@ -353,6 +354,10 @@ typedef struct {
   int64_t x_stride;     /* the same of x and dx */
   int64_t h_stride;     /* the same of h and dh */
 } spec_scan_params;
+
+/* Bytes of workspace the two calls below need on the current device (0 if the
+ * parameters are invalid, or without a GPU). */
+size_t spec_scan_workspace_size(const spec_scan_params *p);
 
 /* Gated linear recurrence over sequences, a sequential head that trains by a
  * scan (beside spec_cycle_rnn's, which is sequential by its form):
