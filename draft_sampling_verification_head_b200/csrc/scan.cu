@@ -149,6 +149,12 @@ SPEC_DEV void gate_of(RawOf<T, V> raw, Vec<V>& f, Vec<V>& i) {
   i = e * f;
 }
 
+// Waits for the launch before, where this one was allowed to start early.
+SPEC_DEV void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+SPEC_DEV void grid_dependency_release() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 struct ScanArgs {
   spec_scan_params p;
   const void* gate;
@@ -170,23 +176,28 @@ struct ScanArgs {
   int jobs;     // sequences x tiles (x segments)
   int nseg;     // segments per sequence, where a warp has one of its own
   int seg;      // steps per segment, a multiple of kChunk
-  float2* maps;   // [B][nseg][D] a segment's map
-  float* starts;  // [B][nseg][D] the value a segment starts from
+  float2* maps;    // [B][nseg][D] a segment's map
+  float2* groups;  // [B][nseg / kSoloWarps][D] the map of a CTA's segments
+  float* first;    // [B][D] h0 (or dh_last), which the last segment may write over
 };
 
-// Where a job of a warp of its own lies: a sequence, a tile of channels, and a
-// segment of the steps (all of them where nothing is split).
+// Where a job lies: a sequence, a tile of channels and a segment of the steps
+// (all of them where nothing is split).  `pos` numbers the segments in the order
+// of the recurrence, which the gradient runs backwards.
 struct Place {
-  int b, ct, seg, t0, t1;
+  int b, ct, pos, t0, t1;
+  SPEC_DEV int ch0() const { return t0 / kChunk; }
+  SPEC_DEV int ch1() const { return t1 > t0 ? (t1 + kChunk - 1) / kChunk : ch0(); }
 };
-SPEC_DEV Place place_of(const ScanArgs& a, int job, int width) {
+SPEC_DEV Place place_of(const ScanArgs& a, int job, int width, bool grad) {
   Place p;
-  p.seg = job % a.nseg;
+  p.pos = job % a.nseg;
   job /= a.nseg;
   p.b = job / a.tiles;
   p.ct = (job % a.tiles) * width;
-  p.t0 = p.seg * a.seg;
-  p.t1 = min(p.t0 + a.seg, a.p.T);
+  const int64_t t0 = (int64_t)(grad ? a.nseg - 1 - p.pos : p.pos) * a.seg;
+  p.t0 = (int)min(t0, (int64_t)a.p.T);
+  p.t1 = (int)min(t0 + a.seg, (int64_t)a.p.T);
   return p;
 }
 
@@ -245,7 +256,9 @@ struct Joiner {
   uint64_t full[2];
 };
 template <int V>
-struct Joiner<V, 1> {};
+struct Joiner<V, 1> {
+  float2 part[kSoloWarps][32 * V];
+};
 
 constexpr uint64_t kJoinPolls = 1ull << 22;  // about 4 s
 
@@ -367,6 +380,49 @@ SPEC_DEV void state_store(float* p, Vec<V> x) {
   for (int v = 0; v < V; ++v) p[v] = x.get(v);
 }
 
+// The value a segment of a split sequence starts from: the first one taken through
+// the maps of the groups before the segment's own (a run of them per warp,
+// joined in order) and of the segments before it in its group.  The CTA's warps
+// hold the consecutive segments of one group.
+template <int V>
+SPEC_DEV Vec<V> segment_start(const ScanArgs& a, Joiner<V, 1>& sm, const Place& at, int c,
+                              bool on) {
+  const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31, D = a.p.D;
+  const int group = at.pos / kSoloWarps, per = (group + kSoloWarps - 1) / kSoloWarps;
+  const int g0 = min(wid * per, group), g1 = min(g0 + per, group);
+  const int64_t grow = (int64_t)at.b * (a.nseg / kSoloWarps) * D + c;
+  const int64_t mrow = ((int64_t)at.b * a.nseg + group * kSoloWarps) * D + c;
+  float s[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    float2 own[kSoloWarps - 1];
+#pragma unroll
+    for (int w = 0; w < kSoloWarps - 1; ++w)
+      own[w] = on && w < wid ? __ldcg(a.maps + mrow + (int64_t)w * D + v) : make_float2(1.f, 0.f);
+    float ma = 1.f, mc = 0.f;
+#pragma unroll 8
+    for (int g = g0; g < g1; ++g) {
+      const float2 m = on ? __ldcg(a.groups + grow + (int64_t)g * D + v) : make_float2(1.f, 0.f);
+      ma *= m.x;
+      mc = fmaf(m.x, mc, m.y);
+    }
+    sm.part[wid][v * 32 + lane] = make_float2(ma, mc);
+    __syncthreads();
+    s[v] = on ? __ldcg(a.first + (int64_t)at.b * D + c + v) : 0.f;
+#pragma unroll
+    for (int w = 0; w < kSoloWarps; ++w) {
+      const float2 m = sm.part[w][v * 32 + lane];
+      s[v] = fmaf(m.x, s[v], m.y);
+    }
+#pragma unroll
+    for (int w = 0; w < kSoloWarps - 1; ++w) s[v] = fmaf(own[w].x, s[v], own[w].y);
+  }
+  if constexpr (V == 2)
+    return Vec<2>::of(s[0], s[1]);
+  else
+    return {s[0]};
+}
+
 // Forward.  W > 1: a cluster per job (a sequence's tile of 32 V channels) walks
 // the steps in windows of cluster * W pieces.  W = 1: a warp per job, a window is
 // one piece and nothing is joined.  The next window's inputs are requested
@@ -378,28 +434,26 @@ struct ScanShared {
 };
 
 template <typename T, int V, int W>
-__global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), W == 16 ? 1 : 2)
+__global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), 2)
     k_scan(ScanArgs a) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   ScanShared<T, V, W>& sm = *reinterpret_cast<ScanShared<T, V, W>*>(smem_raw);
   const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int C = W == 1 ? 1 : a.cluster, rank = blockIdx.x % C, warp = W == 1 ? 0 : wid;
   const int job = W == 1 ? blockIdx.x * kSoloWarps + wid : blockIdx.x / C;
-  if (job >= a.jobs) return;  // W = 1 only: whole warps, and no barrier follows
-  const Place at = place_of(a, job, 32 * V);
+  if (job >= a.jobs) return;  // whole warps, only where no barrier follows (W = 1, unsplit)
+  const Place at = place_of(a, job, 32 * V, false);
   const int b = at.b, ct = at.ct, c = ct + lane * V;
   const int D = a.p.D, Tn = a.p.T;
   const bool on = c < D;  // pairs are only taken where D is even
   const int n = len_of(a.len, b, Tn, a.hdr,
-                       ct == 0 && at.seg == 0 && rank == 0 && warp == 0 && lane == 0);
+                       ct == 0 && at.pos == 0 && rank == 0 && warp == 0 && lane == 0);
   const int64_t row0 = (int64_t)b * Tn;
   const T* gp = (const T*)a.gate + row0 * a.p.gate_stride + ct;
   const T* xp = (const T*)a.x + row0 * a.p.x_stride + ct;
   T* hp = (T*)a.h + row0 * a.p.h_stride + c;
   const int nch = (Tn + kChunk - 1) / kChunk;
-  Vec<V> carry = a.nseg > 1
-                     ? state_load<V>(a.starts + ((int64_t)b * a.nseg + at.seg) * D + c, on)
-                     : state_load<V>(a.h0 + (int64_t)b * D + c, a.h0 && on);
+  Vec<V> carry = state_load<V>(a.h0 + (int64_t)b * D + c, a.h0 && on);
 
   const int window = C * W * kChunk;
   int t0 = at.t0 + (rank * W + warp) * kChunk;
@@ -412,6 +466,12 @@ __global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), W == 16 ? 1 : 
   };
   request(t0);
   join_init<V, W>(sm.joiner, C);
+  if constexpr (W == 1) {
+    if (a.nseg > 1) {
+      grid_dependency_wait();  // the maps; the inputs above do not depend on them
+      carry = segment_start<V>(a, sm.joiner, at, c, on);
+    }
+  }
   const int nwin = (at.t1 - at.t0 + window - 1) / window;
   for (int win = 0; win < nwin; ++win, t0 += window) {
     Vec<V> f[kChunk], z[kChunk], ma = Vec<V>::all(1.f), mc = Vec<V>::all(0.f);
@@ -461,7 +521,7 @@ __global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), W == 16 ? 1 : 
     }
     __syncwarp();
   }
-  if (a.h_last && at.seg == a.nseg - 1 && rank == 0 && warp == 0 && on)
+  if (a.h_last && at.pos == a.nseg - 1 && rank == 0 && warp == 0 && on)
     state_store<V>(a.h_last + (int64_t)b * D + c, carry);
 }
 
@@ -476,7 +536,7 @@ struct GradShared {
 };
 
 template <typename T, int V, int W>
-__global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), W == 16 ? 1 : 2)
+__global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), 2)
     k_scan_grad(ScanArgs a) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   GradShared<T, V, W>& sm = *reinterpret_cast<GradShared<T, V, W>*>(smem_raw);
@@ -484,13 +544,13 @@ __global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), W == 16 ? 1 : 
   const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int C = W == 1 ? 1 : a.cluster, rank = blockIdx.x % C, warp = W == 1 ? 0 : wid;
   const int job = W == 1 ? blockIdx.x * kSoloWarps + wid : blockIdx.x / C;
-  if (job >= a.jobs) return;  // W = 1 only: whole warps, and no barrier follows
-  const Place at = place_of(a, job, 32 * V);
+  if (job >= a.jobs) return;  // whole warps, only where no barrier follows (W = 1, unsplit)
+  const Place at = place_of(a, job, 32 * V, true);
   const int b = at.b, ct = at.ct, c = ct + lane * V;
   const int D = a.p.D, Tn = a.p.T;
   const bool on = c < D;
   const int n = len_of(a.len, b, Tn, a.hdr,
-                       ct == 0 && at.seg == 0 && rank == 0 && warp == 0 && lane == 0);
+                       ct == 0 && at.pos == 0 && rank == 0 && warp == 0 && lane == 0);
   const int64_t row0 = (int64_t)b * Tn;
   const T* gp = (const T*)a.gate + row0 * a.p.gate_stride + ct;
   const T* xp = (const T*)a.x + row0 * a.p.x_stride + ct;
@@ -498,12 +558,10 @@ __global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), W == 16 ? 1 : 
   T* dgp = (T*)a.dgate + row0 * a.p.gate_stride + c;
   T* dxp = (T*)a.dx + row0 * a.p.x_stride + c;
   const int nch = (Tn + kChunk - 1) / kChunk;
-  Vec<V> carry = a.nseg > 1
-                     ? state_load<V>(a.starts + ((int64_t)b * a.nseg + at.seg) * D + c, on)
-                     : state_load<V>(a.dh_last + (int64_t)b * D + c, a.dh_last && on);
+  Vec<V> carry = state_load<V>(a.dh_last + (int64_t)b * D + c, a.dh_last && on);
 
   const int window = C * W;  // in pieces
-  const int ch0 = at.t0 / kChunk, ch1 = (at.t1 + kChunk - 1) / kChunk;
+  const int ch0 = at.ch0(), ch1 = at.ch1();
   int ch = ch1 - 1 - (rank * W + warp);
   Vec<V> s0;
   auto request = [&](int q, int par) {
@@ -518,6 +576,12 @@ __global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), W == 16 ? 1 : 
   };
   request(ch, 0);
   join_init<V, W>(sm.joiner, C);
+  if constexpr (W == 1) {
+    if (a.nseg > 1) {
+      grid_dependency_wait();  // the maps; the inputs above do not depend on them
+      carry = segment_start<V>(a, sm.joiner, at, c, on);
+    }
+  }
   const int nwin = (ch1 - ch0 + window - 1) / window;
   for (int win = 0; win < nwin; ++win, ch -= window) {
     const int t0 = ch * kChunk, left = ch < ch0 ? 0 : n - t0, par = win & 1;
@@ -577,40 +641,45 @@ __global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), W == 16 ? 1 : 
     }
     __syncwarp();
   }
-  if (a.dh0 && at.seg == 0 && rank == 0 && warp == 0 && on)
+  if (a.dh0 && at.pos == a.nseg - 1 && rank == 0 && warp == 0 && on)
     state_store<V>(a.dh0 + (int64_t)b * D + c, carry);
 }
 
 // ----------------------------------------------------------------------------
 // Long sequences of few channels: even a cluster per job leaves most of the GPU
-// idle, so the steps are split into segments, a warp each.  One pass reduces
-// every segment to its map, a small kernel joins the maps into the values that
-// the segments start from, and the kernels above run with a warp per segment.
-// The inputs of the recurrence are read twice, the second time mostly from L2.
+// idle, so the steps are split into segments, a warp each.  A first pass reduces
+// every segment, and every CTA's group of them, to its map; the kernels above
+// then run with a warp per segment, which they start from the joined maps of
+// what lies before.  The inputs of the recurrence are read twice, the second
+// time mostly from L2.
 // ----------------------------------------------------------------------------
-constexpr int kMapWarps = 4;
+template <typename T, int V>
+struct MapShared {
+  Piece<T, V> gate[kSoloWarps][2], other[kSoloWarps][2];
+  float2 part[kSoloWarps][32 * V];
+};
 
 template <typename T, int V, bool kGrad>
-__global__ void __launch_bounds__(32 * kMapWarps) k_scan_maps(ScanArgs a) {
-  __shared__ Piece<T, V> gate[kMapWarps][2], other[kMapWarps][2];
+__global__ void __launch_bounds__(32 * kSoloWarps, 2) k_scan_maps(ScanArgs a) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  MapShared<T, V>& sm = *reinterpret_cast<MapShared<T, V>*>(smem_raw);
+  grid_dependency_release();
   const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int job = blockIdx.x * kMapWarps + wid;
-  if (job >= a.jobs) return;
-  const Place at = place_of(a, job, 32 * V);
+  const Place at = place_of(a, blockIdx.x * kSoloWarps + wid, 32 * V, kGrad);
   const int b = at.b, ct = at.ct, c = ct + lane * V, D = a.p.D;
   const int n = len_of(a.len, b, a.p.T, a.hdr, false);
   const int64_t row0 = (int64_t)b * a.p.T;
   const int64_t stride = kGrad ? a.p.h_stride : a.p.x_stride;
   const T* gp = (const T*)a.gate + row0 * a.p.gate_stride + ct;
   const T* op = (const T*)(kGrad ? a.dh : a.x) + row0 * stride + ct;
-  const int ch0 = at.t0 / kChunk, ch1 = (at.t1 + kChunk - 1) / kChunk;
+  const int ch0 = at.ch0(), ch1 = at.ch1();
   // the pieces in the order of the recurrence
   auto piece = [&](int q) { return kGrad ? ch1 - 1 - q : ch0 + q; };
   auto request = [&](int q) {
     const int t = piece(q) * kChunk;
     if (q < ch1 - ch0 && t < n) {
-      fetch(gate[wid][q & 1], gp + (int64_t)t * a.p.gate_stride, a.p.gate_stride, n - t, D - ct, a.wide);
-      fetch(other[wid][q & 1], op + (int64_t)t * stride, stride, n - t, D - ct, a.wide);
+      fetch(sm.gate[wid][q & 1], gp + (int64_t)t * a.p.gate_stride, a.p.gate_stride, n - t, D - ct, a.wide);
+      fetch(sm.other[wid][q & 1], op + (int64_t)t * stride, stride, n - t, D - ct, a.wide);
     }
     cp_async_commit();
   };
@@ -623,8 +692,8 @@ __global__ void __launch_bounds__(32 * kMapWarps) k_scan_maps(ScanArgs a) {
     const int left = n - piece(q) * kChunk;
     auto step = [&](int k) {
       Vec<V> f, i;
-      gate_of<T, V>(gate[wid][q & 1].at[k][lane], f, i);
-      const Vec<V> o = raw_value<T, V>(other[wid][q & 1].at[k][lane]);
+      gate_of<T, V>(sm.gate[wid][q & 1].at[k][lane], f, i);
+      const Vec<V> o = raw_value<T, V>(sm.other[wid][q & 1].at[k][lane]);
       ma = ma * f;
       if constexpr (kGrad)
         mc = f * (mc + o);
@@ -639,46 +708,28 @@ __global__ void __launch_bounds__(32 * kMapWarps) k_scan_maps(ScanArgs a) {
     }
     __syncwarp();
   }
-  if (c < D) {
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      a.maps[((int64_t)b * a.nseg + at.seg) * D + c + v] = make_float2(ma.get(v), mc.get(v));
-  }
-}
-
-constexpr int kJoinWarps = 16;
-
-// One CTA per sequence and 32 channels; a warp takes a run of segments.
-__global__ void __launch_bounds__(32 * kJoinWarps) k_scan_starts(ScanArgs a, bool grad) {
-  __shared__ float2 part[kJoinWarps][32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int D = a.p.D, tiles = (D + 31) / 32, b = blockIdx.x / tiles;
-  const int c = (blockIdx.x % tiles) * 32 + lane;
-  const bool on = c < D;
-  const int per = (a.nseg + kJoinWarps - 1) / kJoinWarps;
-  const int q0 = min(warp * per, a.nseg), q1 = min(q0 + per, a.nseg);
-  const int64_t row = (int64_t)b * a.nseg;
-  // the segments in the order of the recurrence
-  auto at = [&](int q) { return (row + (grad ? a.nseg - 1 - q : q)) * D + c; };
-  float ma = 1.f, mc = 0.f;
-#pragma unroll 8
-  for (int q = q0; q < q1; ++q) {
-    const float2 m = on ? a.maps[at(q)] : make_float2(1.f, 0.f);
-    ma *= m.x;
-    mc = fmaf(m.x, mc, m.y);
-  }
-  part[warp][lane] = make_float2(ma, mc);
-  __syncthreads();
-  const float* first = grad ? a.dh_last : a.h0;
-  float s = first && on ? first[(int64_t)b * D + c] : 0.f;
-  for (int w = 0; w < warp; ++w) s = fmaf(part[w][lane].x, s, part[w][lane].y);
-#pragma unroll 8
-  for (int q = q0; q < q1; ++q) {
-    if (on) {
-      const float2 m = a.maps[at(q)];
-      a.starts[at(q)] = s;
-      s = fmaf(m.x, s, m.y);
+  for (int v = 0; v < V; ++v) {
+    const float2 m = make_float2(ma.get(v), mc.get(v));
+    sm.part[wid][v * 32 + lane] = m;
+    if (at.pos == 0 && c < D) {
+      const float* first = kGrad ? a.dh_last : a.h0;
+      const int64_t e = (int64_t)b * D + c + v;
+      a.first[e] = first ? first[e] : 0.f;
     }
+    if (c < D) a.maps[((int64_t)b * a.nseg + at.pos) * D + c + v] = m;
+  }
+  __syncthreads();
+  if (wid < V && ct + lane * V + wid < D) {
+    float ta = 1.f, tc = 0.f;
+#pragma unroll
+    for (int w = 0; w < kSoloWarps; ++w) {
+      const float2 m = sm.part[w][wid * 32 + lane];
+      ta *= m.x;
+      tc = fmaf(m.x, tc, m.y);
+    }
+    a.groups[((int64_t)b * (a.nseg / kSoloWarps) + at.pos / kSoloWarps) * D + c + wid] =
+        make_float2(ta, tc);
   }
 }
 
@@ -711,6 +762,13 @@ int segment_steps(const spec_scan_params& p, int64_t jobs, int num_sms) {
   return (int)std::max<int64_t>((steps + kChunk - 1) / kChunk * kChunk, kMinSegment);
 }
 
+// Dynamic shared memory beyond the default needs leave.
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t bytes) {
+  if (bytes <= 48 * 1024) return cudaSuccess;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
 template <typename T, int V, int W>
 cudaError_t launch(ScanArgs& a, bool grad, int num_sms, cudaStream_t st) {
   const int64_t jobs = jobs_of(a.p, V) * a.nseg;
@@ -726,23 +784,28 @@ cudaError_t launch(ScanArgs& a, bool grad, int num_sms, cudaStream_t st) {
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
   void (*kernel)(ScanArgs) = grad ? k_scan_grad<T, V, W> : k_scan<T, V, W>;
   const size_t smem = grad ? sizeof(GradShared<T, V, W>) : sizeof(ScanShared<T, V, W>);
-  if (smem > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
+  const cudaError_t e = allow_smem(kernel, smem);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(32 * (W == 1 ? kSoloWarps : W));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = C;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = C;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = a.nseg > 1 ? 2 : 1;  // behind its maps' launch it may start early
   return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+// Segments per sequence, whole groups of them (the last ones may be empty).
+int segments(const spec_scan_params& p, int seg) {
+  const int n = (p.T + seg - 1) / seg;
+  return (n + kSoloWarps - 1) / kSoloWarps * kSoloWarps;
 }
 
 template <typename T, int V, int W>
@@ -759,20 +822,19 @@ cudaError_t by_shape(ScanArgs& a, bool grad, int num_sms, uint8_t* body, cudaStr
     a.seg = a.p.T;
     return launch<T, V, W>(a, grad, num_sms, st);
   }
-  a.nseg = (a.p.T + a.seg - 1) / a.seg;
+  a.nseg = segments(a.p, a.seg);
   a.tiles = (a.p.D + 32 * V - 1) / (32 * V);
-  a.jobs = (int)(jobs_of(a.p, V) * a.nseg);
   a.maps = reinterpret_cast<float2*>(body);
-  a.starts = reinterpret_cast<float*>(a.maps + (size_t)a.p.B * a.nseg * a.p.D);
-  const int grid = (a.jobs + kMapWarps - 1) / kMapWarps;
-  if (grad)
-    k_scan_maps<T, V, true><<<grid, 32 * kMapWarps, 0, st>>>(a);
-  else
-    k_scan_maps<T, V, false><<<grid, 32 * kMapWarps, 0, st>>>(a);
-  k_scan_starts<<<(int)jobs_of(a.p, 1), 32 * kJoinWarps, 0, st>>>(a, grad);
-  const cudaError_t e = cudaGetLastError();
+  a.groups = a.maps + (size_t)a.p.B * a.nseg * a.p.D;
+  a.first = reinterpret_cast<float*>(a.groups + (size_t)a.p.B * (a.nseg / kSoloWarps) * a.p.D);
+  const int grid = (int)(jobs_of(a.p, V) * (a.nseg / kSoloWarps));
+  void (*maps)(ScanArgs) = grad ? k_scan_maps<T, V, true> : k_scan_maps<T, V, false>;
+  cudaError_t e = allow_smem(maps, sizeof(MapShared<T, V>));
   if (e != cudaSuccess) return e;
-  *launches = 3;
+  maps<<<grid, 32 * kSoloWarps, sizeof(MapShared<T, V>), st>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  *launches = 2;
   return launch<T, V, 1>(a, grad, num_sms, st);
 }
 
@@ -783,7 +845,7 @@ cudaError_t dispatch(ScanArgs& a, bool grad, int num_sms, uint8_t* body, cudaStr
   if constexpr (std::is_same<T, __nv_bfloat16>::value) {
     if (pairs_ok(a)) return by_shape<T, 2, 8>(a, grad, num_sms, body, st, launches);
   }
-  return by_shape<T, 1, 16>(a, grad, num_sms, body, st, launches);
+  return by_shape<T, 1, 8>(a, grad, num_sms, body, st, launches);
 }
 
 }  // namespace
@@ -793,8 +855,9 @@ size_t scan_ws_bytes(const spec_scan_params& p, int num_sms) {
   for (int V = 1; V <= (p.dtype == SPEC_BF16 ? 2 : 1); ++V) {  // whichever alignment allows
     const int seg = segment_steps(p, jobs_of(p, V), num_sms);
     if (seg == 0) continue;
-    const size_t nseg = (p.T + seg - 1) / seg;
-    need = std::max(need, (sizeof(float2) + sizeof(float)) * (size_t)p.B * nseg * p.D);
+    const size_t nseg = segments(p, seg);
+    need = std::max(need, (sizeof(float2) * (nseg + nseg / kSoloWarps) + sizeof(float)) *
+                              (size_t)p.B * p.D);
   }
   return need;
 }

@@ -308,6 +308,20 @@ def test_scan_steps_in_place_equal_the_sequence():
     within(state, np64(last), 2 * e)
 
 
+@pytest.mark.parametrize("B,T,D,dtype", [(1, 4099, 40, "bf16"), (2, 2048, 7, "f32"), (2, 700, 64, "bf16")])
+def test_scan_state_in_place_over_long_sequences(B, T, D, dtype):
+    """The last state written over the first one: the same bits as apart."""
+    gate, x, h0, _, _ = scan_inputs(B, T, D, dtype, 12, False)
+    p = sd.ScanParams(B=B, T=T, D=D, dtype=dtype)
+    ws = sd.make_workspace(p)
+    h, last = torch.empty(B, T, D, dtype=DT[dtype], device="cuda"), torch.empty(B, D, device="cuda")
+    h2, state = torch.empty_like(h), h0.clone()
+    sd.gated_scan(p, gate, x, h0, None, h, last, None, ws)
+    sd.gated_scan(p, gate, x, state, None, h2, state, None, ws)
+    assert sd.sync_status(ws) == sd.SPEC_OK
+    assert torch.equal(h, h2) and torch.equal(last, state)
+
+
 def test_scan_no_steps_and_bad_lengths():
     B, D = 3, 9
     p = sd.ScanParams(B=B, T=0, D=D, dtype="f32")
