@@ -1,10 +1,86 @@
 // Scaled lookup of table rows by token, and its gradient.
+//
+// The gradient of a table row is the sum of the rows of all positions that name
+// it.  Few positions (k_grad_direct): a CTA per position looks through all of
+// them, which needs no order.  Many: the positions are sorted by token
+// (k_grad_sort, stable, so positions ascend within a token), equal pieces of the
+// sorted list are summed however the tokens are spread (k_grad_sums), and runs
+// that cross pieces are joined in order (k_grad_join).  Every sum is taken in
+// fp32 in an order that only the tokens fix.
+#include <algorithm>
+
 #include "head_ops.cuh"
 
 namespace specdec {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kCols = 8;  // columns per lane and block of columns
+
+// Eight neighbouring elements (16-byte aligned), or eight `step` apart.
+template <bool kWide>
+SPEC_DEV void load8(const __nv_bfloat16* p, int step, int left, float* x) {
+  if constexpr (kWide) {
+    const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      x[2 * k] = __uint_as_float(u[k] << 16);
+      x[2 * k + 1] = __uint_as_float(u[k] & 0xFFFF0000u);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) x[k] = k * step < left ? load_f(p, k * step) : 0.f;
+  }
+}
+template <bool kWide>
+SPEC_DEV void load8(const float* p, int step, int left, float* x) {
+  if constexpr (kWide) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+    const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  } else {
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) x[k] = k * step < left ? load_f(p, k * step) : 0.f;
+  }
+}
+template <bool kWide>
+SPEC_DEV void store8(__nv_bfloat16* p, int step, int left, const float* x) {
+  if constexpr (kWide) {
+    uint4 w;
+    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&w);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) h[k] = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
+    *reinterpret_cast<uint4*>(p) = w;
+  } else {
+#pragma unroll
+    for (int k = 0; k < kCols; ++k)
+      if (k * step < left) store_f(p, k * step, x[k]);
+  }
+}
+template <bool kWide>
+SPEC_DEV void store8(float* p, int step, int left, const float* x) {
+  if constexpr (kWide) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < kCols; ++k)
+      if (k * step < left) store_f(p, k * step, x[k]);
+  }
+}
+
+// The columns of one lane: `lanes` lanes share a block of kCols * lanes columns.
+template <bool kWide>
+struct Columns {
+  int at, step, left;  // first column, distance, columns of the row from there on (0: none)
+  SPEC_DEV Columns(int block, int lane, int lanes, int D) {
+    at = block * kCols * lanes + (kWide ? lane * kCols : lane);
+    step = kWide ? 1 : lanes;
+    left = max(D - at, 0);
+  }
+};
 
 // rows[i] = scale * table[ids[i]]: one CTA per row.
 template <typename TT, typename TR>
@@ -22,43 +98,502 @@ __global__ void __launch_bounds__(kThreads)
     store_f(dst, c, in ? load_f(src, c) * p.scale : 0.f);
 }
 
-// Zero the table's gradient.
-template <typename TT>
-__global__ void __launch_bounds__(kThreads) k_embed_zero(spec_embed_params p, TT* dtable) {
-  TT* dst = dtable + (int64_t)blockIdx.x * p.table_stride;
-  for (int c = threadIdx.x; c < p.D; c += kThreads) store_f(dst, c, 0.f);
+// ----------------------------------------------------------------------------
+// Gradient
+// ----------------------------------------------------------------------------
+// What goes into a table row: scale * sum, added to what is there or not.
+template <bool kWide, typename TT>
+SPEC_DEV void put_row(const spec_embed_params& p, TT* dtable, int64_t row, const Columns<kWide>& c,
+                      float* acc) {
+  if (c.left <= 0) return;
+  TT* dst = dtable + row * p.table_stride + c.at;
+#pragma unroll
+  for (int k = 0; k < kCols; ++k) acc[k] *= p.scale;
+  if (p.accumulate) {
+    float old[kCols];
+    load8<kWide>((const TT*)dst, c.step, c.left, old);
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) acc[k] += old[k];
+  }
+  store8<kWide>(dst, c.step, c.left, acc);
 }
 
-// One CTA per position: the first position of each token sums the rows of all
-// positions that name it, in ascending order.
-template <typename TT, typename TR>
+// Zero a run of table rows, but for those in a bitmap.
+template <bool kWide, typename TT>
+SPEC_DEV void zero_rows(const spec_embed_params& p, TT* dtable, int64_t v0, int64_t v1,
+                        const uint32_t* skip) {
+  const float zero[kCols] = {};
+  const int lane = threadIdx.x & 31, warps = blockDim.x / 32;
+  for (int64_t v = v0 + threadIdx.x / 32; v < v1; v += warps) {
+    const int k = (int)(v - v0);
+    if (skip && (skip[k >> 5] >> (k & 31) & 1)) continue;
+    for (int block = 0; block * kCols * 32 < p.D; ++block) {
+      const Columns<kWide> c(block, lane, 32, p.D);
+      if (c.left > 0) store8<kWide>(dtable + v * p.table_stride + c.at, c.step, c.left, zero);
+    }
+  }
+}
+
+constexpr int kDirect = 2048;     // most positions that are not sorted
+constexpr int kZeroRows = 1024;   // most table rows a CTA zeroes beside them
+
+// CTAs 0 .. n - 1: the first position of a token sums the rows of all positions
+// that name it; its warps take a run of the positions each.  The CTAs after them
+// zero the rows that no position names.
+template <bool kWide, typename TT, typename TR>
 __global__ void __launch_bounds__(kThreads)
-    k_embed_grad(spec_embed_params p, const int32_t* __restrict__ ids,
-                 const TR* __restrict__ drows, TT* dtable, WsHeader* hdr) {
-  const int i = blockIdx.x;
-  const int id = ids[i];
-  if (id < 0 || id >= p.V) {
-    if (id != -1 && threadIdx.x == 0)
-      report_error(hdr, SPEC_ERR_TOKEN_RANGE, SITE_TOKEN_RANGE, i, id);
+    k_grad_direct(spec_embed_params p, const int32_t* __restrict__ ids,
+                  const TR* __restrict__ drows, TT* dtable, int zero_per, WsHeader* hdr) {
+  __shared__ float part[kThreads / 32][32 * kCols];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = p.n;
+  if ((int)blockIdx.x >= n) {
+    __shared__ uint32_t named[kZeroRows / 32];
+    const int64_t v0 = (int64_t)(blockIdx.x - n) * zero_per, v1 = min(v0 + zero_per, (int64_t)p.V);
+    for (int k = tid; k < kZeroRows / 32; k += kThreads) named[k] = 0;
+    __syncthreads();
+    for (int j = tid; j < n; j += kThreads) {
+      const int64_t k = __ldg(ids + j) - v0;
+      if (k >= 0 && k < v1 - v0) atomicOr(&named[k >> 5], 1u << (k & 31));
+    }
+    __syncthreads();
+    zero_rows<kWide>(p, dtable, v0, v1, named);
     return;
   }
-  bool seen = false;
-  for (int j = threadIdx.x; j < i; j += kThreads) seen |= ids[j] == id;
-  if (__syncthreads_or(seen)) return;
-  TT* dst = dtable + (int64_t)id * p.table_stride;
-  for (int c = threadIdx.x; c < p.D; c += kThreads) {
-    float acc = 0.f;
-    for (int j = i; j < p.n; ++j)
-      if (ids[j] == id) acc += load_f(drows, (int64_t)j * p.row_stride + c);
-    acc *= p.scale;
-    if (p.accumulate) acc += load_f((const TT*)dst, c);
-    store_f(dst, c, acc);
+  const int i = blockIdx.x, id = __ldg(ids + i);
+  if (id < 0 || id >= p.V) {
+    if (id != -1 && tid == 0) report_error(hdr, SPEC_ERR_TOKEN_RANGE, SITE_TOKEN_RANGE, i, id);
+    return;
   }
+  bool before = false, after = false;
+  for (int j = tid; j < n; j += kThreads) {
+    const bool same = __ldg(ids + j) == id;
+    before |= same && j < i;
+    after |= same && j > i;
+  }
+  if (__syncthreads_or(before)) return;
+  const bool alone = !__syncthreads_or(after);
+  if (alone) {  // the common case: one row
+    for (int block = warp; block * kCols * 32 < p.D; block += kThreads / 32) {
+      const Columns<kWide> c(block, lane, 32, p.D);
+      float acc[kCols] = {};
+      if (c.left > 0) load8<kWide>(drows + (int64_t)i * p.row_stride + c.at, c.step, c.left, acc);
+      put_row<kWide>(p, dtable, id, c, acc);
+    }
+    return;
+  }
+  const int per = ((n - i + kThreads / 32 - 1) / (kThreads / 32) + 31) / 32 * 32;
+  const int j0 = i + warp * per, j1 = min(j0 + per, n);
+  for (int block = 0; block * kCols * 32 < p.D; ++block) {
+    const Columns<kWide> c(block, lane, 32, p.D);
+    float acc[kCols] = {};
+    for (int j = j0; j < j1; j += 32) {
+      uint32_t m = __ballot_sync(0xffffffffu, j + lane < j1 && __ldg(ids + min(j + lane, n - 1)) == id);
+      while (m) {  // four rows in flight, added in order
+        float x[4][kCols];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int at = m ? j + __ffs(m) - 1 : -1;
+          m &= m - 1;
+          if (at >= 0 && c.left > 0) {
+            load8<kWide>(drows + (int64_t)at * p.row_stride + c.at, c.step, c.left, x[q]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < kCols; ++k) x[q][k] = 0.f;
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int k = 0; k < kCols; ++k) acc[k] += x[q][k];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) part[warp][k * 32 + lane] = acc[k];
+    __syncthreads();
+    if (warp == 0) {
+#pragma unroll
+      for (int w = 1; w < kThreads / 32; ++w)
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) acc[k] += part[w][k * 32 + lane];
+      put_row<kWide>(p, dtable, id, c, acc);
+    }
+    __syncthreads();
+  }
+}
+
+// ---- Sort ---------------------------------------------------------------------------
+constexpr int kSortThreads = 512;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kDigits = 512;                       // 9 bits a pass
+constexpr int kTile = 2048;                        // positions ranked together
+constexpr int kRounds = kTile / kSortThreads;      // of 32 neighbouring positions per warp
+static_assert(kDigits == kSortThreads, "one thread per digit");
+
+struct SortArgs {
+  spec_embed_params p;
+  const int32_t* ids;
+  int32_t* keys[2];   // tokens; V for positions that name none
+  int32_t* pos[2];
+  int32_t* hist;      // [CTA][digit]
+  int ctas;           // that sort; those after them zero the table
+  int per;            // positions per sorting CTA, a multiple of kTile
+  int passes, bits;   // bits per pass
+  uint64_t spin;
+  WsHeader* hdr;
+};
+
+struct SortShared {
+  int32_t count[kDigits];
+  int32_t base[kDigits];
+  uint16_t warp[kSortWarps][kDigits];
+  int32_t scan[kSortWarps];
+};
+
+// Exclusive prefix sums over the CTA's threads.
+SPEC_DEV int exclusive_scan(int x, int32_t* warps) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int s = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += y;
+  }
+  if (lane == 31) warps[warp] = s;
+  __syncthreads();
+  int before = 0;
+  for (int w = 0; w < warp; ++w) before += warps[w];
+  return before + s - x;
+}
+
+SPEC_DEV int32_t key_at(const SortArgs& a, int pass, int64_t i) {
+  if (pass > 0) return __ldcg(a.keys[pass & 1] + i);
+  const int id = __ldg(a.ids + i);
+  return id >= 0 && id < a.p.V ? id : a.p.V;
+}
+
+// Stable sort by token, 9 bits a pass from the lowest: every CTA counts the
+// digits of its run of positions, and after a barrier of the sorting CTAs knows
+// where its own of each digit go; tile by tile the positions are ranked by
+// ballots and written there.  Sorting is latency, so the other CTAs zero the
+// table meanwhile.  Cooperative launch: the sorting CTAs wait for one another.
+template <bool kWide, typename TT>
+__global__ void __launch_bounds__(kSortThreads, 2) k_grad_sort(SortArgs a, TT* dtable) {
+  __shared__ SortShared sm;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
+  if (cta >= a.ctas) {
+    const int64_t z = gridDim.x - a.ctas, k = cta - a.ctas;
+    zero_rows<kWide>(a.p, dtable, a.p.V * k / z, a.p.V * (k + 1) / z, nullptr);
+    return;
+  }
+  const int64_t n = a.p.n, i0 = min((int64_t)cta * a.per, n), i1 = min(i0 + a.per, n);
+  uint32_t barrier = 0;
+  auto grid_sync = [&]() {
+    barrier += a.ctas;
+    if (a.ctas == 1) {
+      __syncthreads();
+      return true;
+    }
+    __syncthreads();
+    int ok = 1;
+    if (tid == 0) {
+      __threadfence();
+      red_release_add_u32(&a.hdr->bar, 1u);
+      ok = grid_wait_count(a.hdr, &a.hdr->bar, barrier, a.spin, SITE_GRID_BARRIER);
+    }
+    return __syncthreads_and(ok) != 0;
+  };
+  bool ok = true;
+  for (int pass = 0; pass < a.passes && ok; ++pass) {
+    const int shift = pass * a.bits, mask = (1 << a.bits) - 1;
+    sm.count[tid] = 0;
+    __syncthreads();
+    for (int64_t i = i0 + tid; i < i1; i += kSortThreads) {
+      if (pass == 0) {
+        const int id = __ldg(a.ids + i);
+        if ((id < -1 || id >= a.p.V))
+          report_error(a.hdr, SPEC_ERR_TOKEN_RANGE, SITE_TOKEN_RANGE, (int)i, id);
+      }
+      atomicAdd(&sm.count[(key_at(a, pass, i) >> shift) & mask], 1);
+    }
+    __syncthreads();
+    a.hist[(int64_t)cta * kDigits + tid] = sm.count[tid];
+    ok = grid_sync();
+    if (!ok) break;
+    // thread = digit: all positions of it, and those in the CTAs before this one
+    int total = 0, before = 0;
+#pragma unroll 8
+    for (int q = 0; q < a.ctas; ++q) {
+      const int h = __ldcg(a.hist + (int64_t)q * kDigits + tid);
+      if (q < cta) before += h;
+      total += h;
+    }
+    sm.base[tid] = before + exclusive_scan(total, sm.scan);
+    __syncthreads();
+    int32_t* const to_key = a.keys[(pass + 1) & 1];
+    int32_t* const to_pos = a.pos[(pass + 1) & 1];
+    for (int64_t t0 = i0; t0 < i1; t0 += kTile) {
+      for (int k = lane; k < kDigits; k += 32) sm.warp[warp][k] = 0;
+      __syncwarp();
+      int32_t key[kRounds], pos[kRounds];
+      int rank[kRounds];
+#pragma unroll
+      for (int r = 0; r < kRounds; ++r) {
+        const int64_t i = t0 + warp * (kTile / kSortWarps) + r * 32 + lane;
+        key[r] = i < i1 ? key_at(a, pass, i) : -1;
+        pos[r] = pass == 0 ? (int32_t)i : (i < i1 ? __ldcg(a.pos[pass & 1] + i) : 0);
+      }
+#pragma unroll
+      for (int r = 0; r < kRounds; ++r) {
+        const int d = key[r] < 0 ? -1 : (key[r] >> shift) & mask;
+        const uint32_t same = __match_any_sync(0xffffffffu, d);
+        const int lower = __popc(same & ((1u << lane) - 1));
+        rank[r] = d < 0 ? 0 : sm.warp[warp][d] + lower;
+        __syncwarp();
+        if (d >= 0 && lower == 0) sm.warp[warp][d] += (uint16_t)__popc(same);
+        __syncwarp();
+      }
+      __syncthreads();
+      {  // thread = digit: counts of the warps become their offsets
+        int s = 0;
+#pragma unroll
+        for (int w = 0; w < kSortWarps; ++w) {
+          const int c = sm.warp[w][tid];
+          sm.warp[w][tid] = (uint16_t)s;
+          s += c;
+        }
+        sm.count[tid] = s;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int r = 0; r < kRounds; ++r) {
+        if (key[r] < 0) continue;
+        const int d = (key[r] >> shift) & mask;
+        const int64_t to = (int64_t)sm.base[d] + sm.warp[warp][d] + rank[r];
+        to_key[to] = key[r];
+        to_pos[to] = pos[r];
+      }
+      __syncthreads();
+      sm.base[tid] += sm.count[tid];
+      __syncthreads();
+    }
+    if (pass + 1 < a.passes) ok = grid_sync();
+  }
+  if (a.ctas > 1 && tid == 0 && ok) {  // the last CTA leaves the counters at zero
+    __threadfence();
+    if (atomicAdd(&a.hdr->exit_count, 1u) == (uint32_t)a.ctas - 1) {
+      a.hdr->bar = 0;
+      a.hdr->exit_count = 0;
+    }
+  }
+}
+
+// ---- Sums of the sorted list -------------------------------------------------------------
+struct SumArgs {
+  spec_embed_params p;
+  const int32_t* keys;
+  const int32_t* pos;
+  float* part;  // [piece][2][width]: the sum of the run that came in, of the one that goes on
+  int piece;    // positions per piece
+  int pieces, lanes, blocks;
+  int width;    // columns, whole blocks
+};
+
+// `lanes` lanes per piece and block of kCols * lanes columns.
+template <bool kWide, typename TT, typename TR>
+__global__ void __launch_bounds__(kThreads)
+    k_grad_sums(SumArgs a, const TR* __restrict__ drows, TT* dtable) {
+  const int64_t job = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / a.lanes;
+  const int m = (int)(job / a.blocks);
+  if (m >= a.pieces) return;
+  const Columns<kWide> c((int)(job % a.blocks), threadIdx.x % a.lanes, a.lanes, a.p.D);
+  const int n = a.p.n, V = a.p.V, j0 = m * a.piece, j1 = min(j0 + a.piece, n);
+  int cur = __ldg(a.keys + j0);
+  bool came_in = j0 > 0 && __ldg(a.keys + j0 - 1) == cur;
+  float acc[kCols] = {};
+  auto part = [&](int which) {
+    if (c.left <= 0) return;
+    float* q = a.part + ((int64_t)m * 2 + which) * a.width + c.at;
+    store8<kWide>(q, c.step, c.left, acc);
+  };
+  constexpr int kAhead = 8;
+  for (int j = j0; j < j1; j += kAhead) {
+    int key[kAhead];
+    float x[kAhead][kCols];
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) {
+      key[q] = j + q < j1 ? __ldg(a.keys + j + q) : V;
+      if (key[q] < V && c.left > 0) {
+        load8<kWide>(drows + (int64_t)__ldg(a.pos + j + q) * a.p.row_stride + c.at, c.step, c.left, x[q]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) x[q][k] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) {
+      if (j + q >= j1) break;
+      if (key[q] != cur) {  // the run ends here
+        if (came_in)
+          part(0);
+        else
+          put_row<kWide>(a.p, dtable, cur, c, acc);
+        cur = key[q];
+        came_in = false;
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) acc[k] = 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < kCols; ++k) acc[k] += x[q][k];
+    }
+  }
+  if (cur >= V) return;
+  if (came_in)
+    part(0);
+  else if (j1 < n && __ldg(a.keys + j1) == cur)
+    part(1);
+  else
+    put_row<kWide>(a.p, dtable, cur, c, acc);
+}
+
+// One CTA per piece in which a run begins that goes on after it: the sums of
+// its parts, the warps taking a stretch of them each.
+template <bool kWide, typename TT>
+__global__ void __launch_bounds__(kThreads) k_grad_join(SumArgs a, TT* dtable) {
+  __shared__ float sums[kThreads / 32][32 * kCols];
+  const int m = blockIdx.x, n = a.p.n, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t j0 = (int64_t)m * a.piece, j1 = j0 + a.piece;
+  if (j1 >= n) return;
+  const int key = __ldg(a.keys + j1);
+  if (key >= a.p.V || __ldg(a.keys + j1 - 1) != key ||
+      (j0 > 0 && __ldg(a.keys + j0 - 1) == key))
+    return;
+  int more = 0;  // pieces after this one into which the run goes
+  for (int q0 = m + 1;; q0 += kThreads) {
+    const int64_t q = (int64_t)q0 + threadIdx.x;
+    const int got = __syncthreads_count(q < a.pieces && __ldg(a.keys + q * a.piece) == key);
+    more += got;
+    if (got < kThreads) break;
+  }
+  const int per = (more + 1 + kThreads / 32 - 1) / (kThreads / 32);
+  const int q0 = min(warp * per, more + 1), q1 = min(q0 + per, more + 1);
+  for (int block = 0; block * kCols * 32 < a.p.D; ++block) {
+    const Columns<kWide> c(block, lane, 32, a.p.D);
+    float acc[kCols] = {};
+    if (c.left > 0) {
+#pragma unroll 4
+      for (int q = q0; q < q1; ++q) {
+        float x[kCols];
+        load8<kWide>(a.part + ((int64_t)(m + q) * 2 + (q == 0)) * a.width + c.at, c.step, c.left, x);
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) acc[k] += x[k];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) sums[warp][k * 32 + lane] = acc[k];
+    __syncthreads();
+    if (warp == 0) {
+#pragma unroll
+      for (int w = 1; w < kThreads / 32; ++w)
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) acc[k] += sums[w][k * 32 + lane];
+      put_row<kWide>(a.p, dtable, key, c, acc);
+    }
+    __syncthreads();
+  }
+}
+
+// ---- Host ----------------------------------------------------------------------------------
+constexpr int kMaxSortCtas = 64;
+
+struct GradPlan {
+  int ctas, per, passes, bits;         // sort
+  int piece, pieces, lanes, blocks, width;  // sums
+  size_t keys, hist, part, bytes;      // offsets after the two key and position arrays
+};
+
+size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
+
+GradPlan plan_of(const spec_embed_params& p) {
+  GradPlan g = {};
+  const int64_t tiles = ((int64_t)p.n + kTile - 1) / kTile;
+  g.ctas = (int)std::min<int64_t>(tiles, kMaxSortCtas);
+  g.per = (int)((tiles + g.ctas - 1) / g.ctas) * kTile;
+  g.ctas = (int)(((int64_t)p.n + g.per - 1) / g.per);
+  int bits = 1;
+  while (bits < 31 && (int64_t(1) << bits) <= p.V) ++bits;  // the largest key is V
+  if ((int64_t(1) << bits) <= p.V) ++bits;
+  g.passes = (bits + 8) / 9;
+  g.bits = (bits + g.passes - 1) / g.passes;
+  g.lanes = 1;
+  while (g.lanes < 32 && g.lanes * kCols < p.D) g.lanes *= 2;
+  g.blocks = (p.D + g.lanes * kCols - 1) / (g.lanes * kCols);
+  g.width = g.blocks * g.lanes * kCols;
+  // enough pieces to fill the GPU, long enough to be worth their parts
+  g.piece = 16;
+  while (g.piece < 128 && (int64_t)p.n / (2 * g.piece) * g.blocks * g.lanes >= 148 * 2048) g.piece *= 2;
+  g.pieces = (int)(((int64_t)p.n + g.piece - 1) / g.piece);
+  const size_t list = round256(sizeof(int32_t) * (size_t)p.n);
+  g.keys = 4 * list;
+  g.hist = g.keys;
+  g.part = g.hist + round256(sizeof(int32_t) * (size_t)g.ctas * kDigits);
+  g.bytes = g.part + round256(sizeof(float) * 2 * (size_t)g.pieces * g.width);
+  return g;
+}
+
+template <bool kWide, typename TT, typename TR>
+cudaError_t grad(const spec_embed_params& p, const int32_t* ids, const TR* drows, TT* dtable,
+                 uint8_t* body, WsHeader* hdr, int num_sms, cudaStream_t st, int* launches) {
+  if (p.n <= kDirect) {
+    const int want = p.accumulate ? 0 : 4 * num_sms;
+    const int per = want ? (int)std::min<int64_t>(kZeroRows, ((int64_t)p.V + want - 1) / want) : 1;
+    const int zero = want ? (int)(((int64_t)p.V + per - 1) / per) : 0;
+    *launches = 1;
+    k_grad_direct<kWide, TT, TR><<<p.n + zero, kThreads, 0, st>>>(p, ids, drows, dtable, per, hdr);
+    return cudaGetLastError();
+  }
+  const GradPlan g = plan_of(p);
+  const size_t list = g.keys / 4;
+  SortArgs a = {};
+  a.p = p;
+  a.ids = ids;
+  for (int k = 0; k < 2; ++k) {
+    a.keys[k] = reinterpret_cast<int32_t*>(body + k * list);
+    a.pos[k] = reinterpret_cast<int32_t*>(body + (2 + k) * list);
+  }
+  a.hist = reinterpret_cast<int32_t*>(body + g.hist);
+  a.ctas = g.ctas;
+  a.per = g.per;
+  a.passes = g.passes;
+  a.bits = g.bits;
+  a.spin = 4000000ull;
+  a.hdr = hdr;
+  const int grid = p.accumulate ? g.ctas : std::max(2 * num_sms, g.ctas + 1);
+  void* args[] = {&a, &dtable};
+  cudaError_t e = cudaLaunchCooperativeKernel((const void*)k_grad_sort<kWide, TT>, dim3(grid),
+                                              dim3(kSortThreads), args, 0, st);
+  if (e != cudaSuccess) return e;
+  SumArgs s = {};
+  s.p = p;
+  s.keys = a.keys[g.passes & 1];
+  s.pos = a.pos[g.passes & 1];
+  s.part = reinterpret_cast<float*>(body + g.part);
+  s.piece = g.piece;
+  s.pieces = g.pieces;
+  s.lanes = g.lanes;
+  s.blocks = g.blocks;
+  s.width = g.width;
+  const int64_t threads = (int64_t)g.pieces * g.blocks * g.lanes;
+  k_grad_sums<kWide, TT, TR><<<(unsigned)((threads + kThreads - 1) / kThreads), kThreads, 0, st>>>(s, drows, dtable);
+  k_grad_join<kWide, TT><<<g.pieces, kThreads, 0, st>>>(s, dtable);
+  *launches = 3;
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t embed_grad_ws_bytes(const spec_embed_params&) { return 0; }
+size_t embed_grad_ws_bytes(const spec_embed_params& p) {
+  return p.n <= kDirect ? 0 : plan_of(p).bytes;
+}
 
 template <typename TT, typename TR>
 cudaError_t launch_embed(const spec_embed_params& p, const TT* table, const int32_t* ids, TR* rows,
@@ -68,19 +603,21 @@ cudaError_t launch_embed(const spec_embed_params& p, const TT* table, const int3
   return cudaGetLastError();
 }
 
+// Rows of whole 16-byte vectors of both tensors.
+template <typename TT, typename TR>
+bool wide_ok(const spec_embed_params& p, const void* table, const void* rows) {
+  return p.D % kCols == 0 && p.table_stride * sizeof(TT) % 16 == 0 &&
+         p.row_stride * sizeof(TR) % 16 == 0 &&
+         ((reinterpret_cast<uintptr_t>(table) | reinterpret_cast<uintptr_t>(rows)) & 15) == 0;
+}
+
 template <typename TT, typename TR>
 cudaError_t launch_embed_grad(const spec_embed_params& p, const int32_t* ids, const TR* drows,
-                              TT* dtable, uint8_t*, WsHeader* hdr, int, cudaStream_t st,
-                              int* launches) {
-  if (!p.accumulate) {
-    k_embed_zero<TT><<<p.V, kThreads, 0, st>>>(p, dtable);
-    ++*launches;
-  }
-  if (p.n > 0) {
-    k_embed_grad<TT, TR><<<p.n, kThreads, 0, st>>>(p, ids, drows, dtable, hdr);
-    ++*launches;
-  }
-  return cudaGetLastError();
+                              TT* dtable, uint8_t* body, WsHeader* hdr, int num_sms,
+                              cudaStream_t st, int* launches) {
+  return wide_ok<TT, TR>(p, dtable, drows)
+             ? grad<true, TT, TR>(p, ids, drows, dtable, body, hdr, num_sms, st, launches)
+             : grad<false, TT, TR>(p, ids, drows, dtable, body, hdr, num_sms, st, launches);
 }
 
 #define SPEC_INST(TT, TR)                                                                          \
