@@ -17,70 +17,89 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kCols = 8;  // columns per lane and block of columns
 
-// Eight neighbouring elements (16-byte aligned), or eight `step` apart.
-template <bool kWide>
-SPEC_DEV void load8(const __nv_bfloat16* p, int step, int left, float* x) {
-  if constexpr (kWide) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      x[2 * k] = __uint_as_float(u[k] << 16);
-      x[2 * k + 1] = __uint_as_float(u[k] & 0xFFFF0000u);
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < kCols; ++k) x[k] = k * step < left ? load_f(p, k * step) : 0.f;
-  }
-}
-template <bool kWide>
-SPEC_DEV void load8(const float* p, int step, int left, float* x) {
-  if constexpr (kWide) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-    const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-  } else {
-#pragma unroll
-    for (int k = 0; k < kCols; ++k) x[k] = k * step < left ? load_f(p, k * step) : 0.f;
-  }
-}
-template <bool kWide>
-SPEC_DEV void store8(__nv_bfloat16* p, int step, int left, const float* x) {
-  if constexpr (kWide) {
-    uint4 w;
-    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&w);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) h[k] = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
-    *reinterpret_cast<uint4*>(p) = w;
-  } else {
-#pragma unroll
-    for (int k = 0; k < kCols; ++k)
-      if (k * step < left) store_f(p, k * step, x[k]);
-  }
-}
-template <bool kWide>
-SPEC_DEV void store8(float* p, int step, int left, const float* x) {
-  if constexpr (kWide) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-  } else {
-#pragma unroll
-    for (int k = 0; k < kCols; ++k)
-      if (k * step < left) store_f(p, k * step, x[k]);
-  }
-}
-
-// The columns of one lane: `lanes` lanes share a block of kCols * lanes columns.
+// The columns of one lane of `lanes` that share a block of kCols * lanes: two
+// vectors of four (kWide: an instruction of the group covers neighbouring
+// vectors, whole sectors of memory for either type), or eight single ones.
 template <bool kWide>
 struct Columns {
-  int at, step, left;  // first column, distance, columns of the row from there on (0: none)
+  static constexpr int kEach = kWide ? 4 : 1;
+  int at, step, left;  // first column, distance of its vectors, columns from it to the row's end
   SPEC_DEV Columns(int block, int lane, int lanes, int D) {
-    at = block * kCols * lanes + (kWide ? lane * kCols : lane);
-    step = kWide ? 1 : lanes;
-    left = max(D - at, 0);
+    at = block * kCols * lanes + lane * kEach;
+    step = kEach * lanes;
+    left = D - at;
+  }
+  SPEC_DEV bool any() const { return left > 0; }
+};
+
+// One lane's columns of a row as they lie in memory.
+template <bool kWide, typename T>
+struct Raw;
+template <>
+struct Raw<true, __nv_bfloat16> {
+  uint2 v[2];
+  SPEC_DEV void load(const __nv_bfloat16* p, const Columns<true>& c) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      v[k] = k * c.step < c.left ? __ldg(reinterpret_cast<const uint2*>(p + k * c.step)) : make_uint2(0, 0);
+  }
+  SPEC_DEV void clear() { v[0] = v[1] = make_uint2(0, 0); }
+  SPEC_DEV float get(int k) const {
+    const uint32_t w = (k & 2) ? v[k >> 2].y : v[k >> 2].x;
+    return __uint_as_float((k & 1) ? (w & 0xFFFF0000u) : (w << 16));
   }
 };
+template <>
+struct Raw<true, float> {
+  float4 v[2];
+  SPEC_DEV void load(const float* p, const Columns<true>& c) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      v[k] = k * c.step < c.left ? __ldg(reinterpret_cast<const float4*>(p + k * c.step))
+                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  SPEC_DEV void clear() { v[0] = v[1] = make_float4(0.f, 0.f, 0.f, 0.f); }
+  SPEC_DEV float get(int k) const {
+    const float4& q = v[k >> 2];
+    return (k & 3) == 0 ? q.x : (k & 3) == 1 ? q.y : (k & 3) == 2 ? q.z : q.w;
+  }
+};
+template <typename T>
+struct Raw<false, T> {
+  float v[kCols];
+  SPEC_DEV void load(const T* p, const Columns<false>& c) {
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) v[k] = k * c.step < c.left ? load_f(p, k * c.step) : 0.f;
+  }
+  SPEC_DEV void clear() {
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) v[k] = 0.f;
+  }
+  SPEC_DEV float get(int k) const { return v[k]; }
+};
+
+template <bool kWide, typename T>
+SPEC_DEV void store8(T* p, const Columns<kWide>& c, const float* x) {
+  if constexpr (!kWide) {
+#pragma unroll
+    for (int k = 0; k < kCols; ++k)
+      if (k * c.step < c.left) store_f(p, k * c.step, x[k]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (k * c.step >= c.left) continue;
+      const float* q = x + 4 * k;
+      if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float4*>(p + k * c.step) = make_float4(q[0], q[1], q[2], q[3]);
+      } else {
+        uint2 w;
+        reinterpret_cast<__nv_bfloat162*>(&w)[0] = __floats2bfloat162_rn(q[0], q[1]);
+        reinterpret_cast<__nv_bfloat162*>(&w)[1] = __floats2bfloat162_rn(q[2], q[3]);
+        *reinterpret_cast<uint2*>(p + k * c.step) = w;
+      }
+    }
+  }
+}
 
 // rows[i] = scale * table[ids[i]]: one CTA per row.
 template <typename TT, typename TR>
@@ -105,17 +124,17 @@ __global__ void __launch_bounds__(kThreads)
 template <bool kWide, typename TT>
 SPEC_DEV void put_row(const spec_embed_params& p, TT* dtable, int64_t row, const Columns<kWide>& c,
                       float* acc) {
-  if (c.left <= 0) return;
+  if (!c.any()) return;
   TT* dst = dtable + row * p.table_stride + c.at;
 #pragma unroll
   for (int k = 0; k < kCols; ++k) acc[k] *= p.scale;
   if (p.accumulate) {
-    float old[kCols];
-    load8<kWide>((const TT*)dst, c.step, c.left, old);
+    Raw<kWide, TT> old;
+    old.load(dst, c);
 #pragma unroll
-    for (int k = 0; k < kCols; ++k) acc[k] += old[k];
+    for (int k = 0; k < kCols; ++k) acc[k] += old.get(k);
   }
-  store8<kWide>(dst, c.step, c.left, acc);
+  store8<kWide>(dst, c, acc);
 }
 
 // Zero a run of table rows, but for those in a bitmap.
@@ -129,7 +148,7 @@ SPEC_DEV void zero_rows(const spec_embed_params& p, TT* dtable, int64_t v0, int6
     if (skip && (skip[k >> 5] >> (k & 31) & 1)) continue;
     for (int block = 0; block * kCols * 32 < p.D; ++block) {
       const Columns<kWide> c(block, lane, 32, p.D);
-      if (c.left > 0) store8<kWide>(dtable + v * p.table_stride + c.at, c.step, c.left, zero);
+      if (c.any()) store8<kWide>(dtable + v * p.table_stride + c.at, c, zero);
     }
   }
 }
@@ -137,21 +156,24 @@ SPEC_DEV void zero_rows(const spec_embed_params& p, TT* dtable, int64_t v0, int6
 constexpr int kDirect = 2048;     // most positions that are not sorted
 constexpr int kZeroRows = 1024;   // most table rows a CTA zeroes beside them
 
+constexpr int kDirectWarps = 16;
+constexpr int kRun = kDirect / kDirectWarps;  // positions a warp looks through
+
 // CTAs 0 .. n - 1: the first position of a token sums the rows of all positions
-// that name it; its warps take a run of the positions each.  The CTAs after them
-// zero the rows that no position names.
+// that name it; its warps list those of a run of positions each.  The CTAs after
+// them zero the rows that no position names.
 template <bool kWide, typename TT, typename TR>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(32 * kDirectWarps)
     k_grad_direct(spec_embed_params p, const int32_t* __restrict__ ids,
                   const TR* __restrict__ drows, TT* dtable, int zero_per, WsHeader* hdr) {
-  __shared__ float part[kThreads / 32][32 * kCols];
+  constexpr int kAll = 32 * kDirectWarps;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = p.n;
   if ((int)blockIdx.x >= n) {
     __shared__ uint32_t named[kZeroRows / 32];
     const int64_t v0 = (int64_t)(blockIdx.x - n) * zero_per, v1 = min(v0 + zero_per, (int64_t)p.V);
-    for (int k = tid; k < kZeroRows / 32; k += kThreads) named[k] = 0;
+    for (int k = tid; k < kZeroRows / 32; k += kAll) named[k] = 0;
     __syncthreads();
-    for (int j = tid; j < n; j += kThreads) {
+    for (int j = tid; j < n; j += kAll) {
       const int64_t k = __ldg(ids + j) - v0;
       if (k >= 0 && k < v1 - v0) atomicOr(&named[k >> 5], 1u << (k & 31));
     }
@@ -159,60 +181,63 @@ __global__ void __launch_bounds__(kThreads)
     zero_rows<kWide>(p, dtable, v0, v1, named);
     return;
   }
+  __shared__ float part[kDirectWarps][32 * kCols];
+  __shared__ int32_t list[kDirectWarps][kRun];
   const int i = blockIdx.x, id = __ldg(ids + i);
   if (id < 0 || id >= p.V) {
     if (id != -1 && tid == 0) report_error(hdr, SPEC_ERR_TOKEN_RANGE, SITE_TOKEN_RANGE, i, id);
     return;
   }
-  bool before = false, after = false;
-  for (int j = tid; j < n; j += kThreads) {
-    const bool same = __ldg(ids + j) == id;
+  // the warp's run of positions: those that name the token, in order
+  int count = 0;
+  bool before = false;
+#pragma unroll
+  for (int k = 0; k < kRun / 32; ++k) {
+    const int j = warp * kRun + k * 32 + lane;
+    const bool same = j < n && __ldg(ids + j) == id;
     before |= same && j < i;
-    after |= same && j > i;
+    const uint32_t m = __ballot_sync(0xffffffffu, same);
+    if (same) list[warp][count + __popc(m & ((1u << lane) - 1))] = j;
+    count += __popc(m);
   }
   if (__syncthreads_or(before)) return;
-  const bool alone = !__syncthreads_or(after);
+  const bool alone = !__syncthreads_or(count > (warp == i / kRun));
   if (alone) {  // the common case: one row
-    for (int block = warp; block * kCols * 32 < p.D; block += kThreads / 32) {
+    for (int block = warp; block * kCols * 32 < p.D; block += kDirectWarps) {
       const Columns<kWide> c(block, lane, 32, p.D);
-      float acc[kCols] = {};
-      if (c.left > 0) load8<kWide>(drows + (int64_t)i * p.row_stride + c.at, c.step, c.left, acc);
+      Raw<kWide, TR> x;
+      x.load(drows + (int64_t)i * p.row_stride + c.at, c);
+      float acc[kCols];
+#pragma unroll
+      for (int k = 0; k < kCols; ++k) acc[k] = x.get(k);
       put_row<kWide>(p, dtable, id, c, acc);
     }
     return;
   }
-  const int per = ((n - i + kThreads / 32 - 1) / (kThreads / 32) + 31) / 32 * 32;
-  const int j0 = i + warp * per, j1 = min(j0 + per, n);
+  constexpr int kAhead = 8;
   for (int block = 0; block * kCols * 32 < p.D; ++block) {
     const Columns<kWide> c(block, lane, 32, p.D);
     float acc[kCols] = {};
-    for (int j = j0; j < j1; j += 32) {
-      uint32_t m = __ballot_sync(0xffffffffu, j + lane < j1 && __ldg(ids + min(j + lane, n - 1)) == id);
-      while (m) {  // four rows in flight, added in order
-        float x[4][kCols];
+    for (int k0 = 0; k0 < count; k0 += kAhead) {
+      Raw<kWide, TR> x[kAhead];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int at = m ? j + __ffs(m) - 1 : -1;
-          m &= m - 1;
-          if (at >= 0 && c.left > 0) {
-            load8<kWide>(drows + (int64_t)at * p.row_stride + c.at, c.step, c.left, x[q]);
-          } else {
-#pragma unroll
-            for (int k = 0; k < kCols; ++k) x[q][k] = 0.f;
-          }
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int k = 0; k < kCols; ++k) acc[k] += x[q][k];
+      for (int q = 0; q < kAhead; ++q) {
+        if (k0 + q < count)
+          x[q].load(drows + (int64_t)list[warp][k0 + q] * p.row_stride + c.at, c);
+        else
+          x[q].clear();
       }
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q)
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) acc[k] += x[q].get(k);
     }
 #pragma unroll
     for (int k = 0; k < kCols; ++k) part[warp][k * 32 + lane] = acc[k];
     __syncthreads();
     if (warp == 0) {
 #pragma unroll
-      for (int w = 1; w < kThreads / 32; ++w)
+      for (int w = 1; w < kDirectWarps; ++w)
 #pragma unroll
         for (int k = 0; k < kCols; ++k) acc[k] += part[w][k * 32 + lane];
       put_row<kWide>(p, dtable, id, c, acc);
@@ -409,47 +434,65 @@ __global__ void __launch_bounds__(kThreads)
   const int n = a.p.n, V = a.p.V, j0 = m * a.piece, j1 = min(j0 + a.piece, n);
   int cur = __ldg(a.keys + j0);
   bool came_in = j0 > 0 && __ldg(a.keys + j0 - 1) == cur;
+  const int next = j1 < n ? __ldg(a.keys + j1) : V;
   float acc[kCols] = {};
   auto part = [&](int which) {
-    if (c.left <= 0) return;
-    float* q = a.part + ((int64_t)m * 2 + which) * a.width + c.at;
-    store8<kWide>(q, c.step, c.left, acc);
+    if (c.any()) store8<kWide>(a.part + ((int64_t)m * 2 + which) * a.width + c.at, c, acc);
   };
-  constexpr int kAhead = 8;
-  for (int j = j0; j < j1; j += kAhead) {
-    int key[kAhead];
-    float x[kAhead][kCols];
+  // four positions at a time; while one four is added, the rows of the next are
+  // on their way and the positions after those are read (lists end on 256 bytes)
+  constexpr int kFour = 4;
+  int4 key = __ldg(reinterpret_cast<const int4*>(a.keys + j0));
+  int4 pos = __ldg(reinterpret_cast<const int4*>(a.pos + j0));
+  Raw<kWide, TR> x[kFour];
+  int now[kFour];
+  auto fetch = [&](int j) {
+    const int k[kFour] = {key.x, key.y, key.z, key.w}, at[kFour] = {pos.x, pos.y, pos.z, pos.w};
 #pragma unroll
-    for (int q = 0; q < kAhead; ++q) {
-      key[q] = j + q < j1 ? __ldg(a.keys + j + q) : V;
-      if (key[q] < V && c.left > 0) {
-        load8<kWide>(drows + (int64_t)__ldg(a.pos + j + q) * a.p.row_stride + c.at, c.step, c.left, x[q]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < kCols; ++k) x[q][k] = 0.f;
-      }
+    for (int q = 0; q < kFour; ++q) {
+      now[q] = j + q < j1 ? k[q] : V;
+      if (now[q] < V)
+        x[q].load(drows + (int64_t)at[q] * a.p.row_stride + c.at, c);
+      else
+        x[q].clear();
     }
+    if (j + kFour < j1) {
+      key = __ldg(reinterpret_cast<const int4*>(a.keys + j + kFour));
+      pos = __ldg(reinterpret_cast<const int4*>(a.pos + j + kFour));
+    }
+  };
+  fetch(j0);
+  for (int j = j0; j < j1; j += kFour) {
+    Raw<kWide, TR> y[kFour];
+    int own[kFour];
 #pragma unroll
-    for (int q = 0; q < kAhead; ++q) {
-      if (j + q >= j1) break;
-      if (key[q] != cur) {  // the run ends here
-        if (came_in)
-          part(0);
-        else
-          put_row<kWide>(a.p, dtable, cur, c, acc);
-        cur = key[q];
+    for (int q = 0; q < kFour; ++q) {
+      y[q] = x[q];
+      own[q] = now[q];
+    }
+    if (j + kFour < j1) fetch(j + kFour);
+#pragma unroll
+    for (int q = 0; q < kFour; ++q) {
+      if (own[q] != cur) {  // the run ends here, or no run goes on
+        if (cur < V) {
+          if (came_in)
+            part(0);
+          else
+            put_row<kWide>(a.p, dtable, cur, c, acc);
+        }
+        cur = own[q];
         came_in = false;
 #pragma unroll
         for (int k = 0; k < kCols; ++k) acc[k] = 0.f;
       }
 #pragma unroll
-      for (int k = 0; k < kCols; ++k) acc[k] += x[q][k];
+      for (int k = 0; k < kCols; ++k) acc[k] += y[q].get(k);
     }
   }
   if (cur >= V) return;
   if (came_in)
     part(0);
-  else if (j1 < n && __ldg(a.keys + j1) == cur)
+  else if (next == cur)
     part(1);
   else
     put_row<kWide>(a.p, dtable, cur, c, acc);
@@ -479,14 +522,12 @@ __global__ void __launch_bounds__(kThreads) k_grad_join(SumArgs a, TT* dtable) {
   for (int block = 0; block * kCols * 32 < a.p.D; ++block) {
     const Columns<kWide> c(block, lane, 32, a.p.D);
     float acc[kCols] = {};
-    if (c.left > 0) {
-#pragma unroll 4
-      for (int q = q0; q < q1; ++q) {
-        float x[kCols];
-        load8<kWide>(a.part + ((int64_t)(m + q) * 2 + (q == 0)) * a.width + c.at, c.step, c.left, x);
+#pragma unroll 8
+    for (int q = q0; q < q1; ++q) {
+      Raw<kWide, float> x;
+      x.load(a.part + ((int64_t)(m + q) * 2 + (q == 0)) * a.width + c.at, c);
 #pragma unroll
-        for (int k = 0; k < kCols; ++k) acc[k] += x[k];
-      }
+      for (int k = 0; k < kCols; ++k) acc[k] += x.get(k);
     }
 #pragma unroll
     for (int k = 0; k < kCols; ++k) sums[warp][k * 32 + lane] = acc[k];
@@ -530,7 +571,7 @@ GradPlan plan_of(const spec_embed_params& p) {
   g.width = g.blocks * g.lanes * kCols;
   // enough pieces to fill the GPU, long enough to be worth their parts
   g.piece = 16;
-  while (g.piece < 128 && (int64_t)p.n / (2 * g.piece) * g.blocks * g.lanes >= 148 * 2048) g.piece *= 2;
+  while (g.piece < 128 && (int64_t)p.n / (2 * g.piece) * g.blocks * g.lanes >= 148 * 384) g.piece *= 2;
   g.pieces = (int)(((int64_t)p.n + g.piece - 1) / g.piece);
   const size_t list = round256(sizeof(int32_t) * (size_t)p.n);
   g.keys = 4 * list;
@@ -548,7 +589,7 @@ cudaError_t grad(const spec_embed_params& p, const int32_t* ids, const TR* drows
     const int per = want ? (int)std::min<int64_t>(kZeroRows, ((int64_t)p.V + want - 1) / want) : 1;
     const int zero = want ? (int)(((int64_t)p.V + per - 1) / per) : 0;
     *launches = 1;
-    k_grad_direct<kWide, TT, TR><<<p.n + zero, kThreads, 0, st>>>(p, ids, drows, dtable, per, hdr);
+    k_grad_direct<kWide, TT, TR><<<p.n + zero, 32 * kDirectWarps, 0, st>>>(p, ids, drows, dtable, per, hdr);
     return cudaGetLastError();
   }
   const GradPlan g = plan_of(p);
@@ -606,7 +647,7 @@ cudaError_t launch_embed(const spec_embed_params& p, const TT* table, const int3
 // Rows of whole 16-byte vectors of both tensors.
 template <typename TT, typename TR>
 bool wide_ok(const spec_embed_params& p, const void* table, const void* rows) {
-  return p.D % kCols == 0 && p.table_stride * sizeof(TT) % 16 == 0 &&
+  return p.D % 4 == 0 && p.table_stride * sizeof(TT) % 16 == 0 &&
          p.row_stride * sizeof(TR) % 16 == 0 &&
          ((reinterpret_cast<uintptr_t>(table) | reinterpret_cast<uintptr_t>(rows)) & 15) == 0;
 }
