@@ -8,6 +8,7 @@
 // that cross pieces are joined in order (k_grad_join).  Every sum is taken in
 // fp32 in an order that only the tokens fix.
 #include <algorithm>
+#include <type_traits>
 
 #include "head_ops.cuh"
 
@@ -66,16 +67,20 @@ struct Raw<true, float> {
 };
 template <typename T>
 struct Raw<false, T> {
-  float v[kCols];
+  using Bits = std::conditional_t<sizeof(T) == 4, uint32_t, uint16_t>;
+  Bits v[kCols];  // converted when used, so that loads do not wait for one another
   SPEC_DEV void load(const T* p, const Columns<false>& c) {
 #pragma unroll
-    for (int k = 0; k < kCols; ++k) v[k] = k * c.step < c.left ? load_f(p, k * c.step) : 0.f;
+    for (int k = 0; k < kCols; ++k)
+      v[k] = k * c.step < c.left ? __ldg(reinterpret_cast<const Bits*>(p) + k * c.step) : Bits(0);
   }
   SPEC_DEV void clear() {
 #pragma unroll
-    for (int k = 0; k < kCols; ++k) v[k] = 0.f;
+    for (int k = 0; k < kCols; ++k) v[k] = 0;
   }
-  SPEC_DEV float get(int k) const { return v[k]; }
+  SPEC_DEV float get(int k) const {
+    return __uint_as_float(sizeof(T) == 4 ? (uint32_t)v[k] : (uint32_t)v[k] << 16);
+  }
 };
 
 template <bool kWide, typename T>
@@ -163,7 +168,7 @@ constexpr int kRun = kDirect / kDirectWarps;  // positions a warp looks through
 // that name it; its warps list those of a run of positions each.  The CTAs after
 // them zero the rows that no position names.
 template <bool kWide, typename TT, typename TR>
-__global__ void __launch_bounds__(32 * kDirectWarps)
+__global__ void __launch_bounds__(32 * kDirectWarps, 2)
     k_grad_direct(spec_embed_params p, const int32_t* __restrict__ ids,
                   const TR* __restrict__ drows, TT* dtable, int zero_per, WsHeader* hdr) {
   constexpr int kAll = 32 * kDirectWarps;
@@ -221,16 +226,14 @@ __global__ void __launch_bounds__(32 * kDirectWarps)
     for (int k0 = 0; k0 < count; k0 += kAhead) {
       Raw<kWide, TR> x[kAhead];
 #pragma unroll
-      for (int q = 0; q < kAhead; ++q) {
-        if (k0 + q < count)
-          x[q].load(drows + (int64_t)list[warp][k0 + q] * p.row_stride + c.at, c);
-        else
-          x[q].clear();
-      }
-#pragma unroll
       for (int q = 0; q < kAhead; ++q)
+        x[q].load(drows + (int64_t)list[warp][min(k0 + q, count - 1)] * p.row_stride + c.at, c);
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q) {
+        if (k0 + q >= count) break;
 #pragma unroll
         for (int k = 0; k < kCols; ++k) acc[k] += x[q].get(k);
+      }
     }
 #pragma unroll
     for (int k = 0; k < kCols; ++k) part[warp][k * 32 + lane] = acc[k];
