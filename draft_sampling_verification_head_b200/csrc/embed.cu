@@ -263,8 +263,8 @@ struct SortArgs {
   int32_t* keys[2];   // tokens; V for positions that name none
   int32_t* pos[2];
   int32_t* hist;      // [CTA][digit]
-  int ctas;           // that sort; those after them zero the table
-  int per;            // positions per sorting CTA, a multiple of kTile
+  int ctas;
+  int per;            // positions per CTA, a multiple of kTile
   int passes, bits;   // bits per pass
   uint64_t spin;
   WsHeader* hdr;
@@ -293,35 +293,22 @@ SPEC_DEV int exclusive_scan(int x, int32_t* warps) {
   return before + s - x;
 }
 
-SPEC_DEV int32_t key_at(const SortArgs& a, int pass, int64_t i) {
-  if (pass > 0) return __ldcg(a.keys[pass & 1] + i);
-  const int id = __ldg(a.ids + i);
-  return id >= 0 && id < a.p.V ? id : a.p.V;
-}
-
 // Stable sort by token, 9 bits a pass from the lowest: every CTA counts the
-// digits of its run of positions, and after a barrier of the sorting CTAs knows
-// where its own of each digit go; tile by tile the positions are ranked by
-// ballots and written there.  Sorting is latency, so the other CTAs zero the
-// table meanwhile.  Cooperative launch: the sorting CTAs wait for one another.
-template <bool kWide, typename TT>
-__global__ void __launch_bounds__(kSortThreads, 2) k_grad_sort(SortArgs a, TT* dtable) {
+// digits of its run of positions, and after a barrier of the CTAs knows where
+// its own of each digit go; tile by tile the positions are ranked by ballots and
+// written there.  Latency bounds it, so a run of one tile (131072 positions)
+// stays in registers, and the counts of all CTAs are requested at once.
+// Cooperative launch: the CTAs wait for one another.
+__global__ void __launch_bounds__(kSortThreads) k_grad_sort(SortArgs a) {
   __shared__ SortShared sm;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
-  if (cta >= a.ctas) {
-    const int64_t z = gridDim.x - a.ctas, k = cta - a.ctas;
-    zero_rows<kWide>(a.p, dtable, a.p.V * k / z, a.p.V * (k + 1) / z, nullptr);
-    return;
-  }
   const int64_t n = a.p.n, i0 = min((int64_t)cta * a.per, n), i1 = min(i0 + a.per, n);
+  grid_dependency_release();
   uint32_t barrier = 0;
   auto grid_sync = [&]() {
-    barrier += a.ctas;
-    if (a.ctas == 1) {
-      __syncthreads();
-      return true;
-    }
     __syncthreads();
+    if (a.ctas == 1) return true;
+    barrier += a.ctas;
     int ok = 1;
     if (tid == 0) {
       __threadfence();
@@ -330,18 +317,36 @@ __global__ void __launch_bounds__(kSortThreads, 2) k_grad_sort(SortArgs a, TT* d
     }
     return __syncthreads_and(ok) != 0;
   };
+  int32_t key[kRounds], pos[kRounds];
+  auto load = [&](int pass, int64_t t0) {
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+      const int64_t i = t0 + warp * (kTile / kSortWarps) + r * 32 + lane;
+      key[r] = -1;
+      if (i >= i1) continue;
+      if (pass == 0) {
+        const int id = __ldg(a.ids + i);
+        key[r] = id >= 0 && id < a.p.V ? id : a.p.V;
+        pos[r] = (int32_t)i;
+        if (id < -1 || id >= a.p.V)
+          report_error(a.hdr, SPEC_ERR_TOKEN_RANGE, SITE_TOKEN_RANGE, (int)i, id);
+      } else {
+        key[r] = __ldcg(a.keys[pass & 1] + i);
+        pos[r] = __ldcg(a.pos[pass & 1] + i);
+      }
+    }
+  };
+  const bool one_tile = i1 - i0 <= kTile;
   bool ok = true;
   for (int pass = 0; pass < a.passes && ok; ++pass) {
     const int shift = pass * a.bits, mask = (1 << a.bits) - 1;
     sm.count[tid] = 0;
     __syncthreads();
-    for (int64_t i = i0 + tid; i < i1; i += kSortThreads) {
-      if (pass == 0) {
-        const int id = __ldg(a.ids + i);
-        if ((id < -1 || id >= a.p.V))
-          report_error(a.hdr, SPEC_ERR_TOKEN_RANGE, SITE_TOKEN_RANGE, (int)i, id);
-      }
-      atomicAdd(&sm.count[(key_at(a, pass, i) >> shift) & mask], 1);
+    for (int64_t t0 = i0; t0 < i1; t0 += kTile) {
+      load(pass, t0);
+#pragma unroll
+      for (int r = 0; r < kRounds; ++r)
+        if (key[r] >= 0) atomicAdd(&sm.count[(key[r] >> shift) & mask], 1);
     }
     __syncthreads();
     a.hist[(int64_t)cta * kDigits + tid] = sm.count[tid];
@@ -349,11 +354,16 @@ __global__ void __launch_bounds__(kSortThreads, 2) k_grad_sort(SortArgs a, TT* d
     if (!ok) break;
     // thread = digit: all positions of it, and those in the CTAs before this one
     int total = 0, before = 0;
-#pragma unroll 8
-    for (int q = 0; q < a.ctas; ++q) {
-      const int h = __ldcg(a.hist + (int64_t)q * kDigits + tid);
-      if (q < cta) before += h;
-      total += h;
+    for (int q0 = 0; q0 < a.ctas; q0 += 32) {
+      int h[32];
+#pragma unroll
+      for (int q = 0; q < 32; ++q)
+        h[q] = q0 + q < a.ctas ? __ldcg(a.hist + (int64_t)(q0 + q) * kDigits + tid) : 0;
+#pragma unroll
+      for (int q = 0; q < 32; ++q) {
+        before += q0 + q < cta ? h[q] : 0;
+        total += h[q];
+      }
     }
     sm.base[tid] = before + exclusive_scan(total, sm.scan);
     __syncthreads();
@@ -362,14 +372,8 @@ __global__ void __launch_bounds__(kSortThreads, 2) k_grad_sort(SortArgs a, TT* d
     for (int64_t t0 = i0; t0 < i1; t0 += kTile) {
       for (int k = lane; k < kDigits; k += 32) sm.warp[warp][k] = 0;
       __syncwarp();
-      int32_t key[kRounds], pos[kRounds];
+      if (!one_tile) load(pass, t0);
       int rank[kRounds];
-#pragma unroll
-      for (int r = 0; r < kRounds; ++r) {
-        const int64_t i = t0 + warp * (kTile / kSortWarps) + r * 32 + lane;
-        key[r] = i < i1 ? key_at(a, pass, i) : -1;
-        pos[r] = pass == 0 ? (int32_t)i : (i < i1 ? __ldcg(a.pos[pass & 1] + i) : 0);
-      }
 #pragma unroll
       for (int r = 0; r < kRounds; ++r) {
         const int d = key[r] < 0 ? -1 : (key[r] >> shift) & mask;
@@ -424,12 +428,66 @@ struct SumArgs {
   int piece;    // positions per piece
   int pieces, lanes, blocks;
   int width;    // columns, whole blocks
+  int sum_ctas;  // the CTAs after them zero zero_per table rows each
+  int zero_per;
 };
+
+// First place in the sorted list whose token is not below v; a whole warp asks,
+// 32 places at a time.
+SPEC_DEV int lower_bound(const int32_t* keys, int n, int64_t v) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = n;  // the answer is in [lo, hi]
+  while (lo < hi) {
+    const int64_t step = ((int64_t)hi - lo + 32) / 33;
+    const int64_t at = lo + step * (lane + 1) - 1;
+    const bool below = at < hi && __ldg(keys + at) < v;
+    const int k = __popc(__ballot_sync(0xffffffffu, below));  // the list ascends: the first k
+    const int64_t low = lo + step * k;
+    if (k < 32) hi = (int)min((int64_t)hi, low + step - 1);
+    lo = (int)min((int64_t)hi, low);
+  }
+  return lo;
+}
+
+// CTAs after the sums': zero a run of table rows, but for those in the list.
+template <bool kWide, typename TT>
+SPEC_DEV void zero_unnamed(const SumArgs& a, TT* dtable, int cta) {
+  __shared__ uint32_t named[kZeroRows / 32];
+  __shared__ int range[2];
+  const int64_t v0 = (int64_t)cta * a.zero_per, v1 = min(v0 + a.zero_per, (int64_t)a.p.V);
+  const int tid = threadIdx.x, warp = tid >> 5;
+  for (int k = tid; k < kZeroRows / 32; k += kThreads) named[k] = 0;
+  if (warp < 2) {
+    const int at = lower_bound(a.keys, a.p.n, warp ? v1 : v0);
+    if ((tid & 31) == 0) range[warp] = at;
+  }
+  __syncthreads();
+  constexpr int kAhead = 16;  // a token named often fills many places
+  for (int j = range[0] + tid; j < range[1]; j += kAhead * kThreads) {
+    int key[kAhead];
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q)
+      key[q] = __ldg(a.keys + min(j + q * kThreads, range[1] - 1));
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) {
+      const int k = (int)(key[q] - v0);
+      if (q == 0 || key[q] != key[q - 1]) atomicOr(&named[k >> 5], 1u << (k & 31));
+    }
+  }
+  __syncthreads();
+  zero_rows<kWide>(a.p, dtable, v0, v1, named);
+}
 
 // `lanes` lanes per piece and block of kCols * lanes columns.
 template <bool kWide, typename TT, typename TR>
 __global__ void __launch_bounds__(kThreads)
     k_grad_sums(SumArgs a, const TR* __restrict__ drows, TT* dtable) {
+  grid_dependency_release();
+  grid_dependency_wait();
+  if ((int)blockIdx.x >= a.sum_ctas) {
+    zero_unnamed<kWide>(a, dtable, blockIdx.x - a.sum_ctas);
+    return;
+  }
   const int64_t job = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / a.lanes;
   const int m = (int)(job / a.blocks);
   if (m >= a.pieces) return;
@@ -508,6 +566,7 @@ __global__ void __launch_bounds__(kThreads) k_grad_join(SumArgs a, TT* dtable) {
   __shared__ float sums[kThreads / 32][32 * kCols];
   const int m = blockIdx.x, n = a.p.n, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t j0 = (int64_t)m * a.piece, j1 = j0 + a.piece;
+  grid_dependency_wait();
   if (j1 >= n) return;
   const int key = __ldg(a.keys + j1);
   if (key >= a.p.V || __ldg(a.keys + j1 - 1) != key ||
@@ -525,12 +584,20 @@ __global__ void __launch_bounds__(kThreads) k_grad_join(SumArgs a, TT* dtable) {
   for (int block = 0; block * kCols * 32 < a.p.D; ++block) {
     const Columns<kWide> c(block, lane, 32, a.p.D);
     float acc[kCols] = {};
-#pragma unroll 8
-    for (int q = q0; q < q1; ++q) {
-      Raw<kWide, float> x;
-      x.load(a.part + ((int64_t)(m + q) * 2 + (q == 0)) * a.width + c.at, c);
+    constexpr int kAhead = 8;
+    for (int q = q0; q < q1; q += kAhead) {
+      Raw<kWide, float> x[kAhead];
 #pragma unroll
-      for (int k = 0; k < kCols; ++k) acc[k] += x.get(k);
+      for (int r = 0; r < kAhead; ++r) {
+        const int at = min(q + r, q1 - 1);
+        x[r].load(a.part + ((int64_t)(m + at) * 2 + (at == 0)) * a.width + c.at, c);
+      }
+#pragma unroll
+      for (int r = 0; r < kAhead; ++r) {
+        if (q + r >= q1) break;
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) acc[k] += x[r].get(k);
+      }
     }
 #pragma unroll
     for (int k = 0; k < kCols; ++k) sums[warp][k * 32 + lane] = acc[k];
@@ -584,13 +651,17 @@ GradPlan plan_of(const spec_embed_params& p) {
   return g;
 }
 
+// Table rows that a CTA zeroes: about four CTAs for every SM.
+int zero_rows_per_cta(const spec_embed_params& p, int num_sms) {
+  return (int)std::min<int64_t>(kZeroRows, ((int64_t)p.V + 4 * num_sms - 1) / (4 * num_sms));
+}
+
 template <bool kWide, typename TT, typename TR>
 cudaError_t grad(const spec_embed_params& p, const int32_t* ids, const TR* drows, TT* dtable,
                  uint8_t* body, WsHeader* hdr, int num_sms, cudaStream_t st, int* launches) {
   if (p.n <= kDirect) {
-    const int want = p.accumulate ? 0 : 4 * num_sms;
-    const int per = want ? (int)std::min<int64_t>(kZeroRows, ((int64_t)p.V + want - 1) / want) : 1;
-    const int zero = want ? (int)(((int64_t)p.V + per - 1) / per) : 0;
+    const int per = zero_rows_per_cta(p, num_sms);
+    const int zero = p.accumulate ? 0 : (int)(((int64_t)p.V + per - 1) / per);
     *launches = 1;
     k_grad_direct<kWide, TT, TR><<<p.n + zero, 32 * kDirectWarps, 0, st>>>(p, ids, drows, dtable, per, hdr);
     return cudaGetLastError();
@@ -611,9 +682,8 @@ cudaError_t grad(const spec_embed_params& p, const int32_t* ids, const TR* drows
   a.bits = g.bits;
   a.spin = 4000000ull;
   a.hdr = hdr;
-  const int grid = p.accumulate ? g.ctas : std::max(2 * num_sms, g.ctas + 1);
-  void* args[] = {&a, &dtable};
-  cudaError_t e = cudaLaunchCooperativeKernel((const void*)k_grad_sort<kWide, TT>, dim3(grid),
+  void* args[] = {&a};
+  cudaError_t e = cudaLaunchCooperativeKernel((const void*)k_grad_sort, dim3(g.ctas),
                                               dim3(kSortThreads), args, 0, st);
   if (e != cudaSuccess) return e;
   SumArgs s = {};
@@ -627,10 +697,16 @@ cudaError_t grad(const spec_embed_params& p, const int32_t* ids, const TR* drows
   s.blocks = g.blocks;
   s.width = g.width;
   const int64_t threads = (int64_t)g.pieces * g.blocks * g.lanes;
-  k_grad_sums<kWide, TT, TR><<<(unsigned)((threads + kThreads - 1) / kThreads), kThreads, 0, st>>>(s, drows, dtable);
-  k_grad_join<kWide, TT><<<g.pieces, kThreads, 0, st>>>(s, dtable);
+  const int64_t sum_ctas = (threads + kThreads - 1) / kThreads;
+  s.zero_per = zero_rows_per_cta(p, num_sms);
+  const int64_t zero = p.accumulate ? 0 : ((int64_t)p.V + s.zero_per - 1) / s.zero_per;
+  if (sum_ctas + zero > INT32_MAX) return cudaErrorInvalidValue;
+  s.sum_ctas = (int)sum_ctas;
+  e = launch_after(k_grad_sums<kWide, TT, TR>, (unsigned)(sum_ctas + zero), kThreads, 0, st, s,
+                   drows, dtable);
+  if (e != cudaSuccess) return e;
   *launches = 3;
-  return cudaGetLastError();
+  return launch_after(k_grad_join<kWide, TT>, g.pieces, kThreads, 0, st, s, dtable);
 }
 
 }  // namespace

@@ -21,6 +21,31 @@ SPEC_DEV void report_error(WsHeader* h, int32_t code, int32_t site, int32_t a, i
 SPEC_DEV void store_f(float* p, int64_t i, float v) { p[i] = v; }
 SPEC_DEV void store_f(__nv_bfloat16* p, int64_t i, float v) { p[i] = __float2bfloat16_rn(v); }
 
+// A launch that was allowed to start early waits here for the one before it;
+// a kernel lets the launch after it start early.
+SPEC_DEV void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+SPEC_DEV void grid_dependency_release() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Launch a kernel that calls grid_dependency_wait before it touches anything
+// the launch before it writes: its CTAs may be set up while that one ends.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem,
+                         cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 // ---- Scaled lookup and its gradient -------------------------------------------
 size_t embed_grad_ws_bytes(const spec_embed_params& p);
 template <typename TT, typename TR>

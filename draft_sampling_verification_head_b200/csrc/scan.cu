@@ -149,12 +149,6 @@ SPEC_DEV void gate_of(RawOf<T, V> raw, Vec<V>& f, Vec<V>& i) {
   i = e * f;
 }
 
-// Waits for the launch before, where this one was allowed to start early.
-SPEC_DEV void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-SPEC_DEV void grid_dependency_release() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
 struct ScanArgs {
   spec_scan_params p;
   const void* gate;
