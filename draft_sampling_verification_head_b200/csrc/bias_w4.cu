@@ -36,9 +36,11 @@ __host__ __device__ __forceinline__ int packed_byte(int k) {
 // into three bf16 parts, which together hold all its 24 bits, as columns of
 // their own, so its products are exact as well.
 //
-// Bytes bound it: the codes pass through once.  The features are split over up
-// to 8 warps of a CTA, which keeps its tail short, and joined in order in shared
-// memory.
+// Bytes bound it: the codes pass through once, two blocks of 128 features ahead
+// of the products in registers.  The block of X that a CTA's warps multiply by is
+// laid out in shared memory as the fragments they read, one block ahead.  Where
+// the vocabulary gives too few CTAs, the warps split the features and join their
+// sums in order.
 // ----------------------------------------------------------------------------
 constexpr int kWarps = kThreads / 32;
 
@@ -70,164 +72,208 @@ SPEC_DEV uint32_t part_of(const uint4& w, int i) {
   return i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w;
 }
 
-// Eight features of one row of X, as pairs (k, k + 4): bf16, or part s (0 the
-// leading one) of an fp32.
-SPEC_DEV void x_pairs(const __nv_bfloat16* x, bool wide, int, uint32_t* b) {
-  uint32_t u[4];
-  if (wide) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(x));
-    u[0] = w.x, u[1] = w.y, u[2] = w.z, u[3] = w.w;
-  } else {
-    const unsigned short* h = reinterpret_cast<const unsigned short*>(x);
+template <typename T>
+struct XWord {  // eight features of one row of X as they lie in memory
+  static constexpr int kParts = sizeof(T) == 4 ? 3 : 1;  // columns per row of X
+  uint4 v[sizeof(T) / 2];
+  SPEC_DEV void clear() {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) u[k] = (uint32_t)__ldg(h + 2 * k) | (uint32_t)__ldg(h + 2 * k + 1) << 16;
+    for (int k = 0; k < (int)sizeof(T) / 2; ++k) v[k] = make_uint4(0, 0, 0, 0);
   }
-  b[0] = __byte_perm(u[0], u[2], 0x5410);
-  b[1] = __byte_perm(u[0], u[2], 0x7632);
-  b[2] = __byte_perm(u[1], u[3], 0x5410);
-  b[3] = __byte_perm(u[1], u[3], 0x7632);
-}
-SPEC_DEV void x_pairs(const float* x, bool wide, int s, uint32_t* b) {
-  float v[8];
-  if (wide) {
-    const float4 lo = __ldg(reinterpret_cast<const float4*>(x));
-    const float4 hi = __ldg(reinterpret_cast<const float4*>(x) + 1);
-    v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w;
-    v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
-  } else {
+  SPEC_DEV void load(const T* x, bool wide) {
+    if (wide) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = __ldg(x + k);
+      for (int k = 0; k < (int)sizeof(T) / 2; ++k) v[k] = __ldg(reinterpret_cast<const uint4*>(x) + k);
+    } else if constexpr (sizeof(T) == 4) {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(x);
+      v[0] = make_uint4(__ldg(w), __ldg(w + 1), __ldg(w + 2), __ldg(w + 3));
+      v[1] = make_uint4(__ldg(w + 4), __ldg(w + 5), __ldg(w + 6), __ldg(w + 7));
+    } else {
+      const unsigned short* h = reinterpret_cast<const unsigned short*>(x);
+      uint32_t u[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        u[k] = (uint32_t)__ldg(h + 2 * k) | (uint32_t)__ldg(h + 2 * k + 1) << 16;
+      v[0] = make_uint4(u[0], u[1], u[2], u[3]);
+    }
   }
-  uint32_t part[8];
+  // the pairs (k, k + 4) of column `part` (0 holds the leading bits)
+  SPEC_DEV uint4 pairs(int part) const {
+    if constexpr (sizeof(T) == 2) {
+      return make_uint4(__byte_perm(v[0].x, v[0].z, 0x5410), __byte_perm(v[0].x, v[0].z, 0x7632),
+                        __byte_perm(v[0].y, v[0].w, 0x5410), __byte_perm(v[0].y, v[0].w, 0x7632));
+    } else {
+      const uint32_t b[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+      uint32_t c[8];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const uint32_t bits = __float_as_uint(v[k]);
-    const bool finite = (bits & 0x7F800000u) != 0x7F800000u;
-    // cutting keeps the leading 8 bits; the rest is exact, and so is its rest
-    const float r1 = v[k] - __uint_as_float(bits & 0xFFFF0000u);
-    const float r2 = r1 - __uint_as_float(__float_as_uint(r1) & 0xFFFF0000u);
-    const uint32_t head = finite || (bits & 0x007FFFFFu) == 0 ? bits : 0x7FC00000u;
-    const uint32_t tail = __float_as_uint(s == 1 ? r1 : r2);
-    part[k] = s == 0 ? head : finite ? tail : 0u;
+      for (int k = 0; k < 8; ++k) {
+        const bool finite = (b[k] & 0x7F800000u) != 0x7F800000u;
+        // cutting keeps the leading 8 bits; the rest is exact, and so is its rest
+        const float r1 = __uint_as_float(b[k]) - __uint_as_float(b[k] & 0xFFFF0000u);
+        const float r2 = r1 - __uint_as_float(__float_as_uint(r1) & 0xFFFF0000u);
+        const uint32_t head = finite || (b[k] & 0x007FFFFFu) == 0 ? b[k] : 0x7FC00000u;
+        c[k] = part == 0 ? head : finite ? __float_as_uint(part == 1 ? r1 : r2) : 0u;
+      }
+      return make_uint4(__byte_perm(c[0], c[4], 0x7632), __byte_perm(c[1], c[5], 0x7632),
+                        __byte_perm(c[2], c[6], 0x7632), __byte_perm(c[3], c[7], 0x7632));
+    }
   }
-#pragma unroll
-  for (int k = 0; k < 4; ++k) b[k] = __byte_perm(part[k], part[k + 4], 0x7632);
-}
+};
 
-template <typename T, int NT, int MT>
-__global__ void __launch_bounds__(kThreads, MT == 4 ? 1 : 2)
+template <typename T, int NT>
+__host__ __device__ constexpr int rows_of() {  // rows of X that 8 NT columns hold, 16 at most
+  return 8 * NT / XWord<T>::kParts < 16 ? 8 * NT / XWord<T>::kParts : 16;
+}
+constexpr int kTiles = 2;                       // tiles of 16 tokens per warp
+constexpr int kTokens = 16 * kTiles, kPitch = kTokens + 4;
+template <int NT>
+__host__ __device__ constexpr int block_bytes() { return 4 * NT * 32 * 16; }  // one block of X as fragments
+
+template <typename T, int NT>
+__global__ void __launch_bounds__(kThreads, NT <= 3 ? 2 : 1)
     k_bias_w4(spec_w4_params p, const T* __restrict__ x, const int32_t* __restrict__ prev,
               const uint8_t* __restrict__ wq, const void* __restrict__ wscale, const void* base,
               void* out, int split, int wide, WsHeader* hdr) {
-  constexpr int kParts = sizeof(T) == 4 ? 3 : 1;    // columns per row of X
-  constexpr int kRows = 8 * NT / kParts < 16 ? 8 * NT / kParts : 16;
-  constexpr int kTokens = 16 * MT, kPitch = kTokens + 4;
-  extern __shared__ float red[];  // [warp][column][kPitch]
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+  constexpr int kParts = XWord<T>::kParts, kRows = rows_of<T, NT>();
+  // [2][split] blocks of X; at the end [warp][column][kPitch] sums
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ int64_t row_at[kRows];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
   const int ks = warp % split, rg = warp / split;
   const int64_t v0 = ((int64_t)blockIdx.x * (kWarps / split) + rg) * kTokens;
   const int b0 = blockIdx.y * kRows, nb = min(kRows, p.B - b0);
-  const int nkb = (p.r + 127) / 128, kb0 = nkb * ks / split, kb1 = nkb * (ks + 1) / split;
+  const int nkb = (p.r + 127) / 128, steps = (nkb + split - 1) / split;
   const int rowb = nkb * 64, ng = p.r / p.group;
-
-  // this lane's columns of X
-  const T* xr[NT];
-  bool has[NT];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int b = (nt * 8 + g) / kParts;
-    has[nt] = b < nb;
-    int row = has[nt] ? b0 + b : b0;
+  if (tid < nb) {
+    int row = b0 + tid;
     if (prev) {
       row = __ldg(prev + row);
       if (row < 0 || row >= p.x_rows) {
-        if (blockIdx.x == 0 && warp == 0 && has[nt])
-          report_error(hdr, SPEC_ERR_TOKEN_RANGE, SITE_TOKEN_RANGE, b0 + b, row);
+        if (blockIdx.x == 0)
+          report_error(hdr, SPEC_ERR_TOKEN_RANGE, SITE_TOKEN_RANGE, b0 + tid, row);
         row = row < 0 ? 0 : p.x_rows - 1;
       }
     }
-    xr[nt] = x + (int64_t)row * p.x_stride + 8 * t4;
+    row_at[tid] = row * p.x_stride;
   }
 
-  float total[MT][NT][4] = {};
-  if (v0 < p.V) {
-    const int last = (int)min((int64_t)kTokens, p.V - v0) - 1;
-    const uint8_t* w0 = wq + v0 * rowb + t4 * 16;
-    int at[MT][2];  // rows of the tile, the ones past the vocabulary read its last
+  // codes and scales: a warp reads block step * split + ks, two steps ahead
+  const int last = (int)min((int64_t)kTokens, p.V - v0) - 1;  // < 0: no tokens here
+  const uint8_t* w0 = wq + v0 * rowb + t4 * 16;
+  const int per = 128 / p.group;  // groups per block; lane t4 holds the scale of group t4 % per
+  struct Codes {
+    uint4 w[kTiles][2];
+    float s[kTiles][2];
+  };
+  Codes c0, c1, c2;
+  auto request = [&](int step, Codes& c) {
+    const int kb = step * split + ks;
+    if (kb >= nkb || last < 0) return;
+    const int gi = min(kb * per + t4 % per, ng - 1);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      at[mt][0] = min(mt * 16 + g, last);
-      at[mt][1] = min(mt * 16 + g + 8, last);
+    for (int mt = 0; mt < kTiles; ++mt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int at = min(mt * 16 + g + 8 * h, last);  // past the vocabulary: its last row
+        c.w[mt][h] = load_once(w0 + (int64_t)at * rowb + kb * 64);
+        c.s[mt][h] = load_any(wscale, p.scale_dtype, (v0 + at) * ng + gi);
+      }
+  };
+  request(0, c0);
+  request(1, c1);
+
+  // X: word (row, w) of a step's blocks, one per thread and round
+  const int words = split * 16;
+  auto x_at = [&](int step, int e, XWord<T>& q) {
+    const int row = e / words, k = (step * words + e % words) * 8;
+    if (row < nb && k < p.r)
+      q.load(x + row_at[row] + k, wide);
+    else
+      q.clear();
+  };
+  auto x_put = [&](int step, int e, const XWord<T>& q) {
+    const int row = e / words, w = e % words, blk = w >> 4, i = (w >> 2) & 3, j = w & 3;
+    uint4* to = reinterpret_cast<uint4*>(smem) + ((step & 1) * split + blk) * (block_bytes<NT>() / 16);
+#pragma unroll
+    for (int s = 0; s < kParts; ++s) {
+      const int col = row * kParts + s;
+      to[(i * NT + (col >> 3)) * 32 + (col & 7) * 4 + j] = q.pairs(s);
     }
-    uint4 cur[MT][2], nxt[MT][2];
-    float sc[MT][2], sn[MT][2];
-    const int per = 128 / p.group;  // groups per block; lane t4 holds the scale of group t4 % per
-    auto request = [&](int kb, uint4 (&w)[MT][2], float (&s)[MT][2]) {
-      const int gi = min(kb * per + t4 % per, ng - 1);
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          w[mt][h] = load_once(w0 + (int64_t)at[mt][h] * rowb + kb * 64);
-          s[mt][h] = load_any(wscale, p.scale_dtype, (v0 + at[mt][h]) * ng + gi);
-        }
-    };
-    if (kb0 < kb1) request(kb0, cur, sc);
-    for (int kb = kb0; kb < kb1; ++kb) {
-      if (kb + 1 < kb1) request(kb + 1, nxt, sn);
-      float acc[MT][NT][4] = {};
+  };
+  // columns beyond the rows of X stay zero
+  for (int k = tid; k < 2 * split * block_bytes<NT>() / 16; k += kThreads)
+    reinterpret_cast<uint4*>(smem)[k] = make_uint4(0, 0, 0, 0);
+  __syncthreads();
+  const int items = kRows * words;
+  for (int e = tid; e < items; e += kThreads) {
+    XWord<T> q;
+    x_at(0, e, q);
+    if (e / words < nb) x_put(0, e, q);
+  }
+  __syncthreads();
+
+  float total[kTiles][NT][4] = {};
+  for (int step = 0; step < steps; ++step) {
+    request(step + 2, c2);
+    XWord<T> held;  // the next step's first word, stored when this step is done
+    if (step + 1 < steps) x_at(step + 1, tid, held);
+    const int kb = step * split + ks;
+    if (kb < nkb && last >= 0) {
+      const uint4* xs = reinterpret_cast<const uint4*>(smem) +
+                        ((step & 1) * split + ks) * (block_bytes<NT>() / 16) + lane;
+      float acc[kTiles][NT][4] = {};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int k = kb * 128 + 32 * i;
-        if (k < p.r) {
-          uint32_t xb[NT][4];
+        if (kb * 128 + 32 * i >= p.r) break;
+        uint32_t a[kTiles][2][4];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            if (has[nt])
-              x_pairs(xr[nt] + k, wide, (nt * 8 + g) % kParts, xb[nt]);
-            else
-              xb[nt][0] = xb[nt][1] = xb[nt][2] = xb[nt][3] = 0u;
+        for (int mt = 0; mt < kTiles; ++mt) {
+          codes_to_bf16(part_of(c0.w[mt][0], i), a[mt][0]);
+          codes_to_bf16(part_of(c0.w[mt][1], i), a[mt][1]);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint4 xb = xs[(i * NT + nt) * 32];
+#pragma unroll
+          for (int mt = 0; mt < kTiles; ++mt) {
+            mma_bf16(acc[mt][nt], a[mt][0][0], a[mt][1][0], a[mt][0][1], a[mt][1][1], xb.x, xb.y);
+            mma_bf16(acc[mt][nt], a[mt][0][2], a[mt][1][2], a[mt][0][3], a[mt][1][3], xb.z, xb.w);
           }
+        }
+        if ((32 * (i + 1)) % p.group == 0) {  // a group ends
+          const int from = (lane & ~3) + 32 * i / p.group;
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            uint32_t lo[4], hi[4];
-            codes_to_bf16(part_of(cur[mt][0], i), lo);
-            codes_to_bf16(part_of(cur[mt][1], i), hi);
+          for (int mt = 0; mt < kTiles; ++mt) {
+            const float s0 = __shfl_sync(0xffffffffu, c0.s[mt][0], from);
+            const float s1 = __shfl_sync(0xffffffffu, c0.s[mt][1], from);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              mma_bf16(acc[mt][nt], lo[0], hi[0], lo[1], hi[1], xb[nt][0], xb[nt][1]);
-              mma_bf16(acc[mt][nt], lo[2], hi[2], lo[3], hi[3], xb[nt][2], xb[nt][3]);
-            }
-          }
-          if ((32 * (i + 1)) % p.group == 0) {  // a group ends
-            const int from = (lane & ~3) + 32 * i / p.group;
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              const float s0 = __shfl_sync(0xffffffffu, sc[mt][0], from);
-              const float s1 = __shfl_sync(0xffffffffu, sc[mt][1], from);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                total[mt][nt][0] = fmaf(s0, acc[mt][nt][0], total[mt][nt][0]);
-                total[mt][nt][1] = fmaf(s0, acc[mt][nt][1], total[mt][nt][1]);
-                total[mt][nt][2] = fmaf(s1, acc[mt][nt][2], total[mt][nt][2]);
-                total[mt][nt][3] = fmaf(s1, acc[mt][nt][3], total[mt][nt][3]);
-                acc[mt][nt][0] = acc[mt][nt][1] = acc[mt][nt][2] = acc[mt][nt][3] = 0.f;
-              }
+              total[mt][nt][0] = fmaf(s0, acc[mt][nt][0], total[mt][nt][0]);
+              total[mt][nt][1] = fmaf(s0, acc[mt][nt][1], total[mt][nt][1]);
+              total[mt][nt][2] = fmaf(s1, acc[mt][nt][2], total[mt][nt][2]);
+              total[mt][nt][3] = fmaf(s1, acc[mt][nt][3], total[mt][nt][3]);
+              acc[mt][nt][0] = acc[mt][nt][1] = acc[mt][nt][2] = acc[mt][nt][3] = 0.f;
             }
           }
         }
       }
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          cur[mt][h] = nxt[mt][h];
-          sc[mt][h] = sn[mt][h];
-        }
     }
+    if (step + 1 < steps) {
+      if (tid < items && tid / words < nb) x_put(step + 1, tid, held);
+      for (int e = tid + kThreads; e < items; e += kThreads) {
+        XWord<T> q;
+        x_at(step + 1, e, q);
+        if (e / words < nb) x_put(step + 1, e, q);
+      }
+    }
+    c0 = c1;
+    c1 = c2;
+    __syncthreads();
   }
+
+  float* red = reinterpret_cast<float*>(smem);
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
+  for (int mt = 0; mt < kTiles; ++mt)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -236,18 +282,19 @@ __global__ void __launch_bounds__(kThreads, MT == 4 ? 1 : 2)
             total[mt][nt][q];
   __syncthreads();
   // a row group's outputs by its warps, tokens fastest
-  for (int e = ks * 32 + lane; e < nb * kTokens; e += split * 32) {
-    const int b = e / kTokens, t = e % kTokens;
-    if (v0 + t >= p.V) continue;
+  for (int b = ks; b < nb; b += split) {
+    if (lane > last) break;  // kTokens = 32: a lane per token
     float z = 0.f;
     for (int w = 0; w < split; ++w) {
-      const float* r = red + ((rg * split + w) * 8 * NT + b * kParts) * kPitch + t;
+      const float* r = red + ((rg * split + w) * 8 * NT + b * kParts) * kPitch + lane;
       z += kParts == 3 ? (r[2 * kPitch] + r[kPitch]) + r[0] : r[0];
     }
-    if (base) z += load_any(base, p.base_dtype, (int64_t)(b0 + b) * p.base_stride + v0 + t);
-    store_any(out, p.out_dtype, (int64_t)(b0 + b) * p.out_stride + v0 + t, z);
+    const int64_t v = v0 + lane;
+    if (base) z += load_any(base, p.base_dtype, (int64_t)(b0 + b) * p.base_stride + v);
+    store_any(out, p.out_dtype, (int64_t)(b0 + b) * p.out_stride + v, z);
   }
 }
+static_assert(kTokens == 32, "the epilogue gives every lane a token");
 
 // One thread per token and 128 features, reading W's columns.
 template <typename T>
@@ -292,19 +339,22 @@ __global__ void __launch_bounds__(kThreads)
 
 }  // namespace
 
-template <typename T, int NT, int MT>
+template <typename T, int NT>
 static cudaError_t product(const spec_w4_params& p, const T* x, const int32_t* prev,
                            const uint8_t* wq, const void* wscale, const void* base, void* out,
-                           WsHeader* hdr, cudaStream_t st) {
-  constexpr int kParts = sizeof(T) == 4 ? 3 : 1;
-  constexpr int kRows = 8 * NT / kParts < 16 ? 8 * NT / kParts : 16;
+                           WsHeader* hdr, int num_sms, cudaStream_t st) {
+  constexpr int kRows = rows_of<T, NT>();
   const int nkb = (p.r + 127) / 128;
+  // warps split the features while the tokens give fewer than two CTAs per SM
   int split = 1;
-  while (split < kWarps && 2 * split <= nkb) split *= 2;
-  const int64_t per = (int64_t)16 * MT * (kWarps / split);
+  while (split < kWarps && 2 * split <= nkb &&
+         ((int64_t)p.V + kTokens * kWarps / split - 1) / (kTokens * kWarps / split) < 2 * num_sms)
+    split *= 2;
+  const int64_t per = (int64_t)kTokens * kWarps / split;
   const int wide = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && p.x_stride * sizeof(T) % 16 == 0;
-  constexpr size_t smem = sizeof(float) * kWarps * 8 * NT * (16 * MT + 4);
-  auto kernel = k_bias_w4<T, NT, MT>;
+  const size_t smem = std::max(sizeof(float) * kWarps * 8 * NT * kPitch,
+                               (size_t)2 * split * block_bytes<NT>());
+  auto kernel = k_bias_w4<T, NT>;
   if (smem > 48 * 1024) {
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -318,20 +368,20 @@ static cudaError_t product(const spec_w4_params& p, const T* x, const int32_t* p
 template <typename T>
 cudaError_t launch_bias_w4(const spec_w4_params& p, const T* x, const int32_t* prev,
                            const uint8_t* wq, const void* wscale, const void* base, void* out,
-                           WsHeader* hdr, int, cudaStream_t st, int* launches) {
+                           WsHeader* hdr, int num_sms, cudaStream_t st, int* launches) {
   if (p.B > 65535) return cudaErrorInvalidValue;
   *launches = 1;
   const int rows = std::min(p.B, 16);
-#define SPEC_W4(NT, MT) return product<T, NT, MT>(p, x, prev, wq, wscale, base, out, hdr, st)
+#define SPEC_W4(NT) return product<T, NT>(p, x, prev, wq, wscale, base, out, hdr, num_sms, st)
   if constexpr (sizeof(T) == 2) {
-    if (rows <= 8) SPEC_W4(1, 4);
-    SPEC_W4(2, 4);
+    if (rows <= 8) SPEC_W4(1);
+    SPEC_W4(2);
   } else {  // three columns a row
-    if (rows <= 2) SPEC_W4(1, 4);
-    if (rows <= 5) SPEC_W4(2, 4);
-    if (rows <= 8) SPEC_W4(3, 2);
-    if (rows <= 10) SPEC_W4(4, 2);
-    SPEC_W4(6, 2);
+    if (rows <= 2) SPEC_W4(1);
+    if (rows <= 5) SPEC_W4(2);
+    if (rows <= 8) SPEC_W4(3);
+    if (rows <= 10) SPEC_W4(4);
+    SPEC_W4(6);
   }
 #undef SPEC_W4
 }
