@@ -47,6 +47,7 @@ _SIGS = {
     "spec_scan_workspace_size": (ctypes.c_size_t, [_P]),
     "spec_gated_scan": (ctypes.c_int, [_P] * 10),
     "spec_gated_scan_grad": (ctypes.c_int, [_P] * 13),
+    "spec_w4_workspace_size": (ctypes.c_size_t, [_P]),
     "spec_bias_w4": (ctypes.c_int, [_P] * 9),
     "spec_w4_quantize": (ctypes.c_int, [_P, _P, ctypes.c_int32, _P, _P, _P]),
     "spec_verify_probs": (ctypes.c_int, [_P] * 13),
@@ -172,6 +173,8 @@ class _Held:
             object.__setattr__(self, k, v)
         if isinstance(self, EmbedParams):
             object.__setattr__(self, "_need", int(lib().spec_embed_workspace_size(self._at)))
+        elif isinstance(self, W4Params):
+            object.__setattr__(self, "_need", int(lib().spec_w4_workspace_size(self._at)))
         elif isinstance(self, ScanParams):
             object.__setattr__(self, "_need", int(lib().spec_scan_workspace_size(self._at)))
         return getattr(self, name)

@@ -37,10 +37,11 @@ __host__ __device__ __forceinline__ int packed_byte(int k) {
 // their own, so its products are exact as well.
 //
 // Bytes bound it: the codes pass through once, two blocks of 128 features ahead
-// of the products in registers.  The block of X that a CTA's warps multiply by is
-// laid out in shared memory as the fragments they read, one block ahead.  Where
-// the vocabulary gives too few CTAs, the warps split the features and join their
-// sums in order.
+// of the products in registers.  X is laid out beforehand (k_w4_x) as the
+// fragments the warps read, and stays in the SMs' first-level caches, so the
+// warps of a CTA need not wait for one another.  Where the vocabulary gives few
+// CTAs, or much work to each, the warps split the features and join their sums
+// in order.
 // ----------------------------------------------------------------------------
 constexpr int kWarps = kThreads / 32;
 
@@ -50,6 +51,14 @@ SPEC_DEV void mma_bf16(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+SPEC_DEV void mma_bf16_zero(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                            uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // Eight codes as four pairs (k, k + 4) of bf16.
@@ -120,158 +129,149 @@ struct XWord {  // eight features of one row of X as they lie in memory
   }
 };
 
-template <typename T, int NT>
-__host__ __device__ constexpr int rows_of() {  // rows of X that 8 NT columns hold, 16 at most
-  return 8 * NT / XWord<T>::kParts < 16 ? 8 * NT / XWord<T>::kParts : 16;
-}
-constexpr int kTiles = 2;                       // tiles of 16 tokens per warp
+template <typename T>
+int rows_of(int NT) { return std::min(8 * NT / XWord<T>::kParts, 16); }  // that 8 NT columns hold
+constexpr int kTiles = 2;  // tiles of 16 tokens per warp
 constexpr int kTokens = 16 * kTiles, kPitch = kTokens + 4;
-template <int NT>
-__host__ __device__ constexpr int block_bytes() { return 4 * NT * 32 * 16; }  // one block of X as fragments
 
-template <typename T, int NT>
+// X as fragments: [row group][block of 128 features][32 features][NT][lane] of
+// 16 bytes, the lane's four pairs of features of its column.  Features past r are
+// zero; columns without a row hold anything, no output is taken from them.
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+    k_w4_x(spec_w4_params p, const T* __restrict__ x, const int32_t* __restrict__ prev, uint4* xf,
+           int NT, int rows, int wide, WsHeader* hdr) {
+  grid_dependency_release();
+  const int words = (p.r + 127) / 128 * 16;  // of eight features
+  const int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const int b = (int)(e / words), w = (int)(e % words);
+  if (b >= p.B) return;
+  int row = b;
+  if (prev) {
+    row = __ldg(prev + b);
+    if (row < 0 || row >= p.x_rows) {
+      if (w == 0) report_error(hdr, SPEC_ERR_TOKEN_RANGE, SITE_TOKEN_RANGE, b, row);
+      row = row < 0 ? 0 : p.x_rows - 1;
+    }
+  }
+  XWord<T> q;
+  q.clear();
+  if (8 * w < p.r) q.load(x + (int64_t)row * p.x_stride + 8 * w, wide);
+  // word w of the row is word w % 4 of 32 features w / 4
+  uint4* to = xf + ((int64_t)(b / rows) * (words / 4) + w / 4) * NT * 32;
+#pragma unroll
+  for (int s = 0; s < XWord<T>::kParts; ++s) {
+    const int col = b % rows * XWord<T>::kParts + s;
+    to[(col >> 3) * 32 + (col & 7) * 4 + (w & 3)] = q.pairs(s);
+  }
+}
+
+template <int NT, int G>
 __global__ void __launch_bounds__(kThreads, NT <= 3 ? 2 : 1)
-    k_bias_w4(spec_w4_params p, const T* __restrict__ x, const int32_t* __restrict__ prev,
-              const uint8_t* __restrict__ wq, const void* __restrict__ wscale, const void* base,
-              void* out, int split, int wide, WsHeader* hdr) {
-  constexpr int kParts = XWord<T>::kParts, kRows = rows_of<T, NT>();
-  // [2][split] blocks of X; at the end [warp][column][kPitch] sums
-  extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ int64_t row_at[kRows];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+    k_bias_w4(spec_w4_params p, const uint4* xf, const uint8_t* __restrict__ wq,
+              const void* __restrict__ wscale, const void* base, void* out, int split, int parts,
+              int rows) {
+  constexpr int kPer = 128 / G;  // groups per block; lane t4 holds the scale of group t4 % kPer
+  extern __shared__ __align__(16) float red[];  // [warp][column][kPitch]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
   const int ks = warp % split, rg = warp / split;
   const int64_t v0 = ((int64_t)blockIdx.x * (kWarps / split) + rg) * kTokens;
-  const int b0 = blockIdx.y * kRows, nb = min(kRows, p.B - b0);
-  const int nkb = (p.r + 127) / 128, steps = (nkb + split - 1) / split;
-  const int rowb = nkb * 64, ng = p.r / p.group;
-  if (tid < nb) {
-    int row = b0 + tid;
-    if (prev) {
-      row = __ldg(prev + row);
-      if (row < 0 || row >= p.x_rows) {
-        if (blockIdx.x == 0)
-          report_error(hdr, SPEC_ERR_TOKEN_RANGE, SITE_TOKEN_RANGE, b0 + tid, row);
-        row = row < 0 ? 0 : p.x_rows - 1;
-      }
-    }
-    row_at[tid] = row * p.x_stride;
-  }
-
-  // codes and scales: a warp reads block step * split + ks, two steps ahead
+  const int b0 = blockIdx.y * rows, nb = min(rows, p.B - b0);
+  const int nkb = (p.r + 127) / 128, rowb = nkb * 64, ng = p.r / G;
+  const int kb0 = nkb * ks / split, kb1 = nkb * (ks + 1) / split;
   const int last = (int)min((int64_t)kTokens, p.V - v0) - 1;  // < 0: no tokens here
-  const uint8_t* w0 = wq + v0 * rowb + t4 * 16;
-  const int per = 128 / p.group;  // groups per block; lane t4 holds the scale of group t4 % per
+
   struct Codes {
     uint4 w[kTiles][2];
     float s[kTiles][2];
   };
-  Codes c0, c1, c2;
-  auto request = [&](int step, Codes& c) {
-    const int kb = step * split + ks;
-    if (kb >= nkb || last < 0) return;
-    const int gi = min(kb * per + t4 % per, ng - 1);
+  const uint8_t* wp = wq + v0 * rowb + t4 * 16;
+  int w_at[kTiles][2], s_at[kTiles][2];  // past the vocabulary: its last row
+#pragma unroll
+  for (int mt = 0; mt < kTiles; ++mt)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int at = max(min(mt * 16 + g + 8 * h, last), 0);
+      w_at[mt][h] = at * rowb;
+      s_at[mt][h] = at * ng;
+    }
+  auto request = [&](int kb, Codes& c) {
+    if (kb >= kb1 || last < 0) return;
+    const uint8_t* w = wp + (int64_t)kb * 64;
+    const int64_t s = v0 * ng + min(kb * kPer + t4 % kPer, ng - 1);
 #pragma unroll
     for (int mt = 0; mt < kTiles; ++mt)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int at = min(mt * 16 + g + 8 * h, last);  // past the vocabulary: its last row
-        c.w[mt][h] = load_once(w0 + (int64_t)at * rowb + kb * 64);
-        c.s[mt][h] = load_any(wscale, p.scale_dtype, (v0 + at) * ng + gi);
-      }
-  };
-  request(0, c0);
-  request(1, c1);
-
-  // X: word (row, w) of a step's blocks, one per thread and round
-  const int words = split * 16;
-  auto x_at = [&](int step, int e, XWord<T>& q) {
-    const int row = e / words, k = (step * words + e % words) * 8;
-    if (row < nb && k < p.r)
-      q.load(x + row_at[row] + k, wide);
-    else
-      q.clear();
-  };
-  auto x_put = [&](int step, int e, const XWord<T>& q) {
-    const int row = e / words, w = e % words, blk = w >> 4, i = (w >> 2) & 3, j = w & 3;
-    uint4* to = reinterpret_cast<uint4*>(smem) + ((step & 1) * split + blk) * (block_bytes<NT>() / 16);
+      for (int h = 0; h < 2; ++h) c.w[mt][h] = load_once(w + w_at[mt][h]);
+    if (p.scale_dtype == SPEC_BF16) {
 #pragma unroll
-    for (int s = 0; s < kParts; ++s) {
-      const int col = row * kParts + s;
-      to[(i * NT + (col >> 3)) * 32 + (col & 7) * 4 + j] = q.pairs(s);
+      for (int mt = 0; mt < kTiles; ++mt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          c.s[mt][h] = load_f((const __nv_bfloat16*)wscale + s, s_at[mt][h]);
+    } else {
+#pragma unroll
+      for (int mt = 0; mt < kTiles; ++mt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) c.s[mt][h] = load_f((const float*)wscale + s, s_at[mt][h]);
     }
   };
-  // columns beyond the rows of X stay zero
-  for (int k = tid; k < 2 * split * block_bytes<NT>() / 16; k += kThreads)
-    reinterpret_cast<uint4*>(smem)[k] = make_uint4(0, 0, 0, 0);
-  __syncthreads();
-  const int items = kRows * words;
-  for (int e = tid; e < items; e += kThreads) {
-    XWord<T> q;
-    x_at(0, e, q);
-    if (e / words < nb) x_put(0, e, q);
-  }
-  __syncthreads();
+  Codes c0, c1;
+  request(kb0, c0);
+  request(kb0 + 1, c1);
+  grid_dependency_wait();  // X's fragments
 
+  const uint4* xs = xf + (int64_t)blockIdx.y * nkb * (4 * NT * 32) + lane;
   float total[kTiles][NT][4] = {};
-  for (int step = 0; step < steps; ++step) {
-    request(step + 2, c2);
-    XWord<T> held;  // the next step's first word, stored when this step is done
-    if (step + 1 < steps) x_at(step + 1, tid, held);
-    const int kb = step * split + ks;
-    if (kb < nkb && last >= 0) {
-      const uint4* xs = reinterpret_cast<const uint4*>(smem) +
-                        ((step & 1) * split + ks) * (block_bytes<NT>() / 16) + lane;
-      float acc[kTiles][NT][4] = {};
+  auto multiply = [&](int kb, const Codes& c) {
+    const uint4* xk = xs + kb * (4 * NT * 32);
+    float acc[kTiles][NT][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (kb * 128 + 32 * i >= p.r) break;
-        uint32_t a[kTiles][2][4];
+    for (int i = 0; i < 4; ++i) {
+      uint4 xb[NT];
 #pragma unroll
-        for (int mt = 0; mt < kTiles; ++mt) {
-          codes_to_bf16(part_of(c0.w[mt][0], i), a[mt][0]);
-          codes_to_bf16(part_of(c0.w[mt][1], i), a[mt][1]);
-        }
+      for (int nt = 0; nt < NT; ++nt) xb[nt] = xk[(i * NT + nt) * 32];
+      const bool first = 32 * i % G == 0, ends = 32 * (i + 1) % G == 0;
+#pragma unroll
+      for (int mt = 0; mt < kTiles; ++mt) {
+        uint32_t lo[4], hi[4];
+        codes_to_bf16(part_of(c.w[mt][0], i), lo);
+        codes_to_bf16(part_of(c.w[mt][1], i), hi);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const uint4 xb = xs[(i * NT + nt) * 32];
-#pragma unroll
-          for (int mt = 0; mt < kTiles; ++mt) {
-            mma_bf16(acc[mt][nt], a[mt][0][0], a[mt][1][0], a[mt][0][1], a[mt][1][1], xb.x, xb.y);
-            mma_bf16(acc[mt][nt], a[mt][0][2], a[mt][1][2], a[mt][0][3], a[mt][1][3], xb.z, xb.w);
-          }
+          if (first)
+            mma_bf16_zero(acc[mt][nt], lo[0], hi[0], lo[1], hi[1], xb[nt].x, xb[nt].y);
+          else
+            mma_bf16(acc[mt][nt], lo[0], hi[0], lo[1], hi[1], xb[nt].x, xb[nt].y);
+          mma_bf16(acc[mt][nt], lo[2], hi[2], lo[3], hi[3], xb[nt].z, xb[nt].w);
         }
-        if ((32 * (i + 1)) % p.group == 0) {  // a group ends
-          const int from = (lane & ~3) + 32 * i / p.group;
+      }
+      if (ends) {
+        const int from = (lane & ~3) + 32 * i / G;
 #pragma unroll
-          for (int mt = 0; mt < kTiles; ++mt) {
-            const float s0 = __shfl_sync(0xffffffffu, c0.s[mt][0], from);
-            const float s1 = __shfl_sync(0xffffffffu, c0.s[mt][1], from);
+        for (int mt = 0; mt < kTiles; ++mt) {
+          const float s0 = kPer == 1 ? c.s[mt][0] : __shfl_sync(0xffffffffu, c.s[mt][0], from);
+          const float s1 = kPer == 1 ? c.s[mt][1] : __shfl_sync(0xffffffffu, c.s[mt][1], from);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              total[mt][nt][0] = fmaf(s0, acc[mt][nt][0], total[mt][nt][0]);
-              total[mt][nt][1] = fmaf(s0, acc[mt][nt][1], total[mt][nt][1]);
-              total[mt][nt][2] = fmaf(s1, acc[mt][nt][2], total[mt][nt][2]);
-              total[mt][nt][3] = fmaf(s1, acc[mt][nt][3], total[mt][nt][3]);
-              acc[mt][nt][0] = acc[mt][nt][1] = acc[mt][nt][2] = acc[mt][nt][3] = 0.f;
-            }
+          for (int nt = 0; nt < NT; ++nt) {
+            total[mt][nt][0] = fmaf(s0, acc[mt][nt][0], total[mt][nt][0]);
+            total[mt][nt][1] = fmaf(s0, acc[mt][nt][1], total[mt][nt][1]);
+            total[mt][nt][2] = fmaf(s1, acc[mt][nt][2], total[mt][nt][2]);
+            total[mt][nt][3] = fmaf(s1, acc[mt][nt][3], total[mt][nt][3]);
           }
         }
       }
     }
-    if (step + 1 < steps) {
-      if (tid < items && tid / words < nb) x_put(step + 1, tid, held);
-      for (int e = tid + kThreads; e < items; e += kThreads) {
-        XWord<T> q;
-        x_at(step + 1, e, q);
-        if (e / words < nb) x_put(step + 1, e, q);
-      }
+  };
+  if (last >= 0) {
+    for (int kb = kb0; kb < kb1; kb += 2) {
+      multiply(kb, c0);
+      request(kb + 2, c0);
+      if (kb + 1 < kb1) multiply(kb + 1, c1);
+      request(kb + 3, c1);
     }
-    c0 = c1;
-    c1 = c2;
-    __syncthreads();
   }
 
-  float* red = reinterpret_cast<float*>(smem);
 #pragma unroll
   for (int mt = 0; mt < kTiles; ++mt)
 #pragma unroll
@@ -286,8 +286,8 @@ __global__ void __launch_bounds__(kThreads, NT <= 3 ? 2 : 1)
     if (lane > last) break;  // kTokens = 32: a lane per token
     float z = 0.f;
     for (int w = 0; w < split; ++w) {
-      const float* r = red + ((rg * split + w) * 8 * NT + b * kParts) * kPitch + lane;
-      z += kParts == 3 ? (r[2 * kPitch] + r[kPitch]) + r[0] : r[0];
+      const float* r = red + ((rg * split + w) * 8 * NT + b * parts) * kPitch + lane;
+      z += parts == 3 ? (r[2 * kPitch] + r[kPitch]) + r[0] : r[0];
     }
     const int64_t v = v0 + lane;
     if (base) z += load_any(base, p.base_dtype, (int64_t)(b0 + b) * p.base_stride + v);
@@ -339,50 +339,73 @@ __global__ void __launch_bounds__(kThreads)
 
 }  // namespace
 
-template <typename T, int NT>
-static cudaError_t product(const spec_w4_params& p, const T* x, const int32_t* prev,
-                           const uint8_t* wq, const void* wscale, const void* base, void* out,
-                           WsHeader* hdr, int num_sms, cudaStream_t st) {
-  constexpr int kRows = rows_of<T, NT>();
+constexpr int kSteps = 16;  // blocks of 128 features a warp goes through, about
+
+// Tiles of eight columns for up to 16 rows of X.
+static int column_tiles(const spec_w4_params& p) {
+  const int rows = std::min(p.B, 16);
+  if (p.dtype == SPEC_BF16) return rows <= 8 ? 1 : 2;
+  return rows <= 2 ? 1 : rows <= 5 ? 2 : rows <= 8 ? 3 : rows <= 10 ? 4 : 6;  // three a row
+}
+
+size_t w4_ws_bytes(const spec_w4_params& p) {
+  const int NT = column_tiles(p);
+  const int rows = p.dtype == SPEC_BF16 ? rows_of<__nv_bfloat16>(NT) : rows_of<float>(NT);
+  return sizeof(uint4) * 32 * 4 * NT * (size_t)((p.r + 127) / 128) * ((p.B + rows - 1) / rows);
+}
+
+template <int NT, int G>
+static cudaError_t product(const spec_w4_params& p, const uint4* xf, const uint8_t* wq,
+                           const void* wscale, const void* base, void* out, int rows, int parts,
+                           int num_sms, cudaStream_t st) {
   const int nkb = (p.r + 127) / 128;
-  // warps split the features while the tokens give fewer than two CTAs per SM
+  // warps split the features while the tokens give fewer than two CTAs per SM,
+  // and until a CTA's work is short, so that the last ones to run end together
   int split = 1;
   while (split < kWarps && 2 * split <= nkb &&
-         ((int64_t)p.V + kTokens * kWarps / split - 1) / (kTokens * kWarps / split) < 2 * num_sms)
+         (nkb / split > kSteps ||
+          ((int64_t)p.V + kTokens * kWarps / split - 1) / (kTokens * kWarps / split) < 2 * num_sms))
     split *= 2;
   const int64_t per = (int64_t)kTokens * kWarps / split;
-  const int wide = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && p.x_stride * sizeof(T) % 16 == 0;
-  const size_t smem = std::max(sizeof(float) * kWarps * 8 * NT * kPitch,
-                               (size_t)2 * split * block_bytes<NT>());
-  auto kernel = k_bias_w4<T, NT>;
+  constexpr size_t smem = sizeof(float) * kWarps * 8 * NT * kPitch;
   if (smem > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = cudaFuncSetAttribute(
+        k_bias_w4<NT, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  kernel<<<dim3((unsigned)((p.V + per - 1) / per), (p.B + kRows - 1) / kRows), kThreads, smem, st>>>(
-      p, x, prev, wq, wscale, base, out, split, wide, hdr);
-  return cudaGetLastError();
+  return launch_after(k_bias_w4<NT, G>,
+                      dim3((unsigned)((p.V + per - 1) / per), (p.B + rows - 1) / rows), kThreads,
+                      smem, st, p, xf, wq, wscale, base, out, split, parts, rows);
 }
 
 template <typename T>
 cudaError_t launch_bias_w4(const spec_w4_params& p, const T* x, const int32_t* prev,
                            const uint8_t* wq, const void* wscale, const void* base, void* out,
-                           WsHeader* hdr, int num_sms, cudaStream_t st, int* launches) {
-  if (p.B > 65535) return cudaErrorInvalidValue;
-  *launches = 1;
-  const int rows = std::min(p.B, 16);
-#define SPEC_W4(NT) return product<T, NT>(p, x, prev, wq, wscale, base, out, hdr, num_sms, st)
-  if constexpr (sizeof(T) == 2) {
-    if (rows <= 8) SPEC_W4(1);
-    SPEC_W4(2);
-  } else {  // three columns a row
-    if (rows <= 2) SPEC_W4(1);
-    if (rows <= 5) SPEC_W4(2);
-    if (rows <= 8) SPEC_W4(3);
-    if (rows <= 10) SPEC_W4(4);
-    SPEC_W4(6);
+                           uint8_t* body, WsHeader* hdr, int num_sms, cudaStream_t st,
+                           int* launches) {
+  const int NT = column_tiles(p), rows = rows_of<T>(NT), parts = XWord<T>::kParts;
+  if ((p.B + rows - 1) / rows > 65535) return cudaErrorInvalidValue;
+  uint4* xf = reinterpret_cast<uint4*>(body);
+  const int wide = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && p.x_stride * sizeof(T) % 16 == 0;
+  const int64_t words = (int64_t)p.B * ((p.r + 127) / 128 * 16);
+  k_w4_x<T><<<(unsigned)((words + kThreads - 1) / kThreads), kThreads, 0, st>>>(p, x, prev, xf, NT,
+                                                                               rows, wide, hdr);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  *launches = 2;
+#define SPEC_W4(NT, G) return product<NT, G>(p, xf, wq, wscale, base, out, rows, parts, num_sms, st)
+#define SPEC_W4_G(NT)                                                                              \
+  if (p.group == 32) SPEC_W4(NT, 32);                                                              \
+  if (p.group == 64) SPEC_W4(NT, 64);                                                              \
+  SPEC_W4(NT, 128)
+  switch (NT) {
+    case 1: SPEC_W4_G(1);
+    case 2: SPEC_W4_G(2);
+    case 3: SPEC_W4_G(3);
+    case 4: SPEC_W4_G(4);
+    default: SPEC_W4_G(6);
   }
+#undef SPEC_W4_G
 #undef SPEC_W4
 }
 
@@ -397,7 +420,7 @@ cudaError_t launch_w4_quantize(const spec_w4_params& p, const T* W, uint8_t* wq,
 #define SPEC_INST(T)                                                                               \
   template cudaError_t launch_bias_w4<T>(const spec_w4_params&, const T*, const int32_t*,          \
                                          const uint8_t*, const void*, const void*, void*,          \
-                                         WsHeader*, int, cudaStream_t, int*);                      \
+                                         uint8_t*, WsHeader*, int, cudaStream_t, int*);            \
   template cudaError_t launch_w4_quantize<T>(const spec_w4_params&, const T*, uint8_t*, void*,     \
                                              cudaStream_t);
 SPEC_INST(float)

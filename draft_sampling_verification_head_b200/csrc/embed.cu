@@ -702,11 +702,11 @@ cudaError_t grad(const spec_embed_params& p, const int32_t* ids, const TR* drows
   const int64_t zero = p.accumulate ? 0 : ((int64_t)p.V + s.zero_per - 1) / s.zero_per;
   if (sum_ctas + zero > INT32_MAX) return cudaErrorInvalidValue;
   s.sum_ctas = (int)sum_ctas;
-  e = launch_after(k_grad_sums<kWide, TT, TR>, (unsigned)(sum_ctas + zero), kThreads, 0, st, s,
+  e = launch_after(k_grad_sums<kWide, TT, TR>, dim3((unsigned)(sum_ctas + zero)), kThreads, 0, st, s,
                    drows, dtable);
   if (e != cudaSuccess) return e;
   *launches = 3;
-  return launch_after(k_grad_join<kWide, TT>, g.pieces, kThreads, 0, st, s, dtable);
+  return launch_after(k_grad_join<kWide, TT>, dim3(g.pieces), kThreads, 0, st, s, dtable);
 }
 
 }  // namespace

@@ -223,6 +223,12 @@ spec_status spec_gated_scan_grad(const spec_scan_params* p, const void* gate, co
   return launched(e, launches);
 }
 
+size_t spec_w4_workspace_size(const spec_w4_params* p) {
+  spec_w4_params d;
+  if (check_w4(p, &d) != SPEC_OK) return 0;
+  return (sizeof(WsHeader) + w4_ws_bytes(d) + 255) & ~size_t(255);
+}
+
 spec_status spec_bias_w4(const spec_w4_params* p, const void* x, const int32_t* prev,
                          const void* wq, const void* wscale, const void* base, void* out, void* ws,
                          spec_stream_t stream) {
@@ -242,9 +248,9 @@ spec_status spec_bias_w4(const spec_w4_params* p, const void* x, const int32_t* 
   const cudaError_t e =
       d.dtype == SPEC_BF16
           ? launch_bias_w4(d, (const __nv_bfloat16*)x, prev, (const uint8_t*)wq, wscale, base, out,
-                           header_of(ws), sms, (cudaStream_t)stream, &launches)
+                           body_of(ws), header_of(ws), sms, (cudaStream_t)stream, &launches)
           : launch_bias_w4(d, (const float*)x, prev, (const uint8_t*)wq, wscale, base, out,
-                           header_of(ws), sms, (cudaStream_t)stream, &launches);
+                           body_of(ws), header_of(ws), sms, (cudaStream_t)stream, &launches);
   return launched(e, launches);
 }
 

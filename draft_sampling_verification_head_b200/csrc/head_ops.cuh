@@ -31,10 +31,10 @@ SPEC_DEV void grid_dependency_release() {
 // Launch a kernel that calls grid_dependency_wait before it touches anything
 // the launch before it writes: its CTAs may be set up while that one ends.
 template <typename... P, typename... A>
-cudaError_t launch_after(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem,
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem,
                          cudaStream_t st, A... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -69,10 +69,12 @@ cudaError_t launch_scan_grad(const spec_scan_params& p, const T* gate, const T* 
                              WsHeader* hdr, int num_sms, cudaStream_t st, int* launches);
 
 // ---- Vocabulary product with 4-bit weights ------------------------------------------
+size_t w4_ws_bytes(const spec_w4_params& p);
 template <typename T>
 cudaError_t launch_bias_w4(const spec_w4_params& p, const T* x, const int32_t* prev,
                            const uint8_t* wq, const void* wscale, const void* base, void* out,
-                           WsHeader* hdr, int num_sms, cudaStream_t st, int* launches);
+                           uint8_t* body, WsHeader* hdr, int num_sms, cudaStream_t st,
+                           int* launches);
 template <typename T>
 cudaError_t launch_w4_quantize(const spec_w4_params& p, const T* W, uint8_t* wq, void* wscale,
                                cudaStream_t st);

@@ -299,12 +299,13 @@ spec_status spec_l2_persist(const void *ptr, size_t bytes, spec_stream_t stream)
  * current device, rows contiguous, any element alignment (16-byte aligned
  * pointers and row strides run faster); strides are in elements, 0 = dense.
  * Outputs may not overlap inputs unless a comment says so.  `workspace` holds
- * at least SPEC_WORKSPACE_MIN bytes (spec_embed_grad and the recurrence: what
- * spec_embed_workspace_size and spec_scan_workspace_size return), zeroed once
- * by spec_workspace_init; errors found on the device go there and are read by
- * spec_sync_status.  spec_embed_grad and the recurrence also keep scratch in
- * it, which calls of one stream may share among themselves, but not with the
- * calls above; the others touch only the status and may share any workspace.
+ * at least SPEC_WORKSPACE_MIN bytes (spec_embed_grad, the recurrence and
+ * spec_bias_w4: what spec_embed_workspace_size, spec_scan_workspace_size and
+ * spec_w4_workspace_size return), zeroed once by spec_workspace_init; errors
+ * found on the device go there and are read by spec_sync_status.  Those three
+ * also keep scratch in it, which calls of one stream may share among
+ * themselves, but not with the calls above; spec_embed and spec_verify_probs
+ * touch only the status and may share any workspace.
  * All calls can be captured into a CUDA graph.  Sums are taken in a fixed
  * order, and equal inputs give equal bits.
  * ------------------------------------------------------------------------- */
@@ -406,6 +407,9 @@ typedef struct {
   int64_t base_stride;  /* between rows of base; 0 = V */
   int64_t out_stride;   /* between rows of out; 0 = V */
 } spec_w4_params;
+
+/* Bytes of workspace spec_bias_w4 needs (0 if the parameters are invalid). */
+size_t spec_w4_workspace_size(const spec_w4_params *p);
 
 /* Vocabulary product with the factor W in 4 bits:
  *   out[b, v] = base[b, v] + sum_k X[b, k] * (code[v, k] - 8) * wscale[v, k / group],

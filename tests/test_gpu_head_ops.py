@@ -587,7 +587,8 @@ def test_a_head_trains_and_decodes_with_them():
     pw = sd.W4Params(B=B, r=D, V=V, group=32, dtype="f32", scale_dtype="f32", base_dtype="f32")
     wq, wscale = sd.w4_quantize(pw, W)
     base, z = rand(g, B, V), torch.empty(B, V, device="cuda")
-    sd.bias_w4(pw, last, None, wq, wscale, base, z, ws)
+    ww = sd.make_workspace(pw)
+    sd.bias_w4(pw, last, None, wq, wscale, base, z, ww)
     wz, mag = H.bias_w4(np64(last), H.w4_unpack(wq.cpu().numpy(), D), np64(wscale), 32, np64(base))
     within(z, wz, (2 * D + 2 * (D // 32) + 2) * U * mag + 1e-38)
 
@@ -606,7 +607,7 @@ def test_a_head_trains_and_decodes_with_them():
     wU, mag, cnt = H.embed_grad(ids.numpy(), wx.reshape(-1, D), 1.0, np.zeros((V, D)))
     eU, _, _ = H.embed_grad(ids.numpy(), ex.reshape(-1, D), 1.0, np.zeros((V, D)))
     within(dU, wU, eU + (cnt[:, None] + 2) * U * mag + 1e-38)
-    for w in (we, ws):
+    for w in (we, ws, ww):
         assert sd.sync_status(w) == sd.SPEC_OK
 
 
@@ -635,7 +636,8 @@ def _every_call(seed, V=3000):
     pw = sd.W4Params(B=3, r=256, V=V, group=64)
     wq, sc = sd.w4_quantize(pw, rand(g, 256, V))
     xw, z = rand(g, 3, 256, dtype="bf16"), torch.empty(3, V, device="cuda")
-    calls.append(("w4", lambda s: sd.bias_w4(pw, xw, None, wq, sc, None, z, wsp, s), [z]))
+    ww = sd.make_workspace(pw)
+    calls.append(("w4", lambda s: sd.bias_w4(pw, xw, None, wq, sc, None, z, ww, s), [z]))
     t, q, dr, ua, ud, _ = probs_inputs(4, 3, V, "f32", "f32", seed)
     t, q, dr, ua, ud = (v.cuda() for v in (t, q, dr, ua, ud))
     pp = sd.ProbsParams(B=4, K=3, V=V)
@@ -696,8 +698,8 @@ def test_two_graphs_share_a_workspace_in_turn():
 
 
 def test_operators_share_a_workspace_with_the_cycle():
-    """All but embed_grad touch only the status: a cycle before and after them
-    on the same workspace gives the same tokens."""
+    """spec_embed and spec_verify_probs touch only the status: a cycle before and
+    after them on the same workspace gives the same tokens."""
     import synth
     w = synth.Workload("hs", B=5, K=3, V=1000, r=64, dtype="bf16", sigma=0.6, seed=71, uw_std=0.3)
     d = {k: v.cuda() for k, v in synth.make(w).items()}
@@ -717,6 +719,10 @@ def test_operators_share_a_workspace_with_the_cycle():
     rows = torch.empty(5, 64, dtype=torch.bfloat16, device="cuda")
     sd.embed(pe, d["U"], ids, rows, ws)
     assert torch.equal(rows, d["U"][:5])
+    t, q, dr, ua, ud, _ = probs_inputs(3, 2, 500, "f32", "f32", 7)
+    out, tau = torch.empty(3, 3, dtype=torch.int32, device="cuda"), torch.empty(3, dtype=torch.int32, device="cuda")
+    sd.verify_probs(sd.ProbsParams(B=3, K=2, V=500), *(v.cuda() for v in (t, q, dr, ua, ud)), None, out, tau,
+                    None, None, ws)
     assert torch.equal(first, cycle())
 
 
