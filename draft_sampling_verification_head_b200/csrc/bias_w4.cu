@@ -65,7 +65,10 @@ SPEC_DEV void mma_bf16_zero(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uin
 SPEC_DEV void codes_to_bf16(uint32_t w, uint32_t* p) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const uint32_t u = ((w >> (4 * k)) & 0x000F000Fu) | 0x43004300u;
+    uint32_t u;  // (w >> 4 k) & 0x000F000F | 0x43004300
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;"
+        : "=r"(u)
+        : "r"(w >> (4 * k)), "r"(0x000F000Fu), "r"(0x43004300u));
     asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(p[k]) : "r"(u), "r"(0x43084308u));  // 136
   }
 }
@@ -183,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 3 ? 2 : 1)
 
   struct Codes {
     uint4 w[kTiles][2];
-    float s[kTiles][2];
+    uint32_t s[kTiles][2];  // as they lie in memory: converted when used, not waited for here
   };
   const uint8_t* wp = wq + v0 * rowb + t4 * 16;
   int w_at[kTiles][2], s_at[kTiles][2];  // past the vocabulary: its last row
@@ -195,6 +198,8 @@ __global__ void __launch_bounds__(kThreads, NT <= 3 ? 2 : 1)
       w_at[mt][h] = at * rowb;
       s_at[mt][h] = at * ng;
     }
+  const bool bf16_scales = p.scale_dtype == SPEC_BF16;
+  auto scale_of = [&](uint32_t raw) { return __uint_as_float(bf16_scales ? raw << 16 : raw); };
   auto request = [&](int kb, Codes& c) {
     if (kb >= kb1 || last < 0) return;
     const uint8_t* w = wp + (int64_t)kb * 64;
@@ -203,19 +208,22 @@ __global__ void __launch_bounds__(kThreads, NT <= 3 ? 2 : 1)
     for (int mt = 0; mt < kTiles; ++mt)
 #pragma unroll
       for (int h = 0; h < 2; ++h) c.w[mt][h] = load_once(w + w_at[mt][h]);
-    if (p.scale_dtype == SPEC_BF16) {
+    if (bf16_scales) {
 #pragma unroll
       for (int mt = 0; mt < kTiles; ++mt)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          c.s[mt][h] = load_f((const __nv_bfloat16*)wscale + s, s_at[mt][h]);
+          c.s[mt][h] = __ldg((const unsigned short*)wscale + s + s_at[mt][h]);
     } else {
 #pragma unroll
       for (int mt = 0; mt < kTiles; ++mt)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) c.s[mt][h] = load_f((const float*)wscale + s, s_at[mt][h]);
+        for (int h = 0; h < 2; ++h) c.s[mt][h] = __ldg((const uint32_t*)wscale + s + s_at[mt][h]);
     }
   };
+  if (base && ks == 0 && lane < nb && last >= 0)  // what the outputs are added to, for the end
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(
+        (const char*)base + ((int64_t)(b0 + lane) * p.base_stride + v0) * (p.base_dtype == SPEC_BF16 ? 2 : 4)));
   Codes c0, c1;
   request(kb0, c0);
   request(kb0 + 1, c1);
@@ -250,8 +258,8 @@ __global__ void __launch_bounds__(kThreads, NT <= 3 ? 2 : 1)
         const int from = (lane & ~3) + 32 * i / G;
 #pragma unroll
         for (int mt = 0; mt < kTiles; ++mt) {
-          const float s0 = kPer == 1 ? c.s[mt][0] : __shfl_sync(0xffffffffu, c.s[mt][0], from);
-          const float s1 = kPer == 1 ? c.s[mt][1] : __shfl_sync(0xffffffffu, c.s[mt][1], from);
+          const float s0 = scale_of(kPer == 1 ? c.s[mt][0] : __shfl_sync(0xffffffffu, c.s[mt][0], from));
+          const float s1 = scale_of(kPer == 1 ? c.s[mt][1] : __shfl_sync(0xffffffffu, c.s[mt][1], from));
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             total[mt][nt][0] = fmaf(s0, acc[mt][nt][0], total[mt][nt][0]);
@@ -281,17 +289,26 @@ __global__ void __launch_bounds__(kThreads, NT <= 3 ? 2 : 1)
         red[(warp * 8 * NT + nt * 8 + 2 * t4 + (q & 1)) * kPitch + mt * 16 + g + 8 * (q >> 1)] =
             total[mt][nt][q];
   __syncthreads();
-  // a row group's outputs by its warps, tokens fastest
-  for (int b = ks; b < nb; b += split) {
-    if (lane > last) break;  // kTokens = 32: a lane per token
-    float z = 0.f;
+  // a row group's outputs by its warps, a lane per token; base is read for all of
+  // them first, since the stores (out may be base) hold later reads back
+  if (lane > last) return;
+  const int64_t v = v0 + lane;
+  float z[16];
+#pragma unroll
+  for (int q = 0; q < 16; ++q) {
+    const int b = ks + q * split;
+    z[q] = base && b < nb ? load_any(base, p.base_dtype, (int64_t)(b0 + b) * p.base_stride + v) : 0.f;
+  }
+#pragma unroll
+  for (int q = 0; q < 16; ++q) {
+    const int b = ks + q * split;
+    if (b >= nb) break;
+    float sum = 0.f;
     for (int w = 0; w < split; ++w) {
       const float* r = red + ((rg * split + w) * 8 * NT + b * parts) * kPitch + lane;
-      z += parts == 3 ? (r[2 * kPitch] + r[kPitch]) + r[0] : r[0];
+      sum += parts == 3 ? (r[2 * kPitch] + r[kPitch]) + r[0] : r[0];
     }
-    const int64_t v = v0 + lane;
-    if (base) z += load_any(base, p.base_dtype, (int64_t)(b0 + b) * p.base_stride + v);
-    store_any(out, p.out_dtype, (int64_t)(b0 + b) * p.out_stride + v, z);
+    store_any(out, p.out_dtype, (int64_t)(b0 + b) * p.out_stride + v, z[q] + sum);
   }
 }
 static_assert(kTokens == 32, "the epilogue gives every lane a token");
