@@ -11,6 +11,8 @@
 // border would have to lie within 2^-52 of the draw to be decided otherwise.
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "head_ops.cuh"
 
 namespace cg = cooperative_groups;
@@ -24,12 +26,19 @@ constexpr int kMaxCluster = 8;
 constexpr int kEach = 8;            // tokens per lane and tile
 constexpr int kTile = 32 * kEach;   // tokens per tile of a warp
 
-// A probability's mass: 0 for NaN, infinities and negative values.
-SPEC_DEV double mass_of(float p) { return p > 0.f && p < INFINITY ? (double)p : 0.0; }
-// Of max(p - q, 0): where p has mass, 0 where the difference is no number.
-SPEC_DEV double residual_of(float p, float q) {
-  const double d = (double)p - (double)q;
-  return p > 0.f && p < INFINITY && d > 0.0 && d < (double)INFINITY ? d : 0.0;
+// What a token adds to the mass: p (0 for NaN, infinities and negative values), or
+// max(p - q, 0) with a q that is NaN or negative counting as 0.  The difference
+// of two fp32 is exact in 64 bits but for exponents 29 apart.
+template <bool kRes>
+SPEC_DEV void add_mass(double& sum, float p, float q) {
+  if constexpr (kRes) {
+    q = fmaxf(q, 0.f);
+    const double d = (double)p - (double)q;
+    if (q < p && p < INFINITY) sum += d;
+  } else {
+    const double d = (double)p;
+    if (p > 0.f && p < INFINITY) sum += d;
+  }
 }
 
 // A lane's tokens v .. v + 7 as they lie in memory.
@@ -99,7 +108,7 @@ struct ProbsArgs {
 template <typename T, typename TD>
 __global__ void __launch_bounds__(kThreads)
     k_verify_probs(ProbsArgs a, const T* __restrict__ target, const TD* __restrict__ draft_probs) {
-  __shared__ double2 chunk[kMaxCluster * kWarps];  // (residual, target) mass of every chunk
+  __shared__ double chunk[2][kMaxCluster * kWarps];  // mass of every chunk of the row
   __shared__ int stop;
   const int C = a.cluster, rank = blockIdx.x % C, b = blockIdx.x / C;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, K = a.p.K, V = a.p.V;
@@ -165,48 +174,70 @@ __global__ void __launch_bounds__(kThreads)
 
   const int tiles = (V + kTile - 1) / kTile, chunks = C * kWarps, mine = rank * kWarps + warp;
   const int t0 = (int)((int64_t)tiles * mine / chunks), t1 = (int)((int64_t)tiles * (mine + 1) / chunks);
-  double res = 0.0, tgt = 0.0;
-  constexpr int kAhead = 2;  // tiles requested together
-  for (int t = t0; t < t1; t += kAhead) {
-    Eight<T> pw[kAhead];
-    Eight<TD> qw[kAhead];
+  // the chunk's mass; two tiles are requested ahead of the two being added
+  auto sum_chunk = [&](auto res) {
+    constexpr bool kRes = decltype(res)::value;
+    constexpr int kAhead = 2;
+    Eight<T> pw[kAhead], pn[kAhead];
+    Eight<TD> qw[kAhead], qn[kAhead];
+    auto fetch = [&](int t, Eight<T>(&pe)[kAhead], Eight<TD>(&qe)[kAhead]) {
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int v = t + k < t1 ? (t + k) * kTile + lane * kEach : V;  // V: nothing, zeros
-      pw[k].load(P, v, V, wide_p);
-      if (!bonus) qw[k].load(Q, v, V, wide_q);
-    }
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-#pragma unroll
-      for (int e = 0; e < kEach; ++e) {
-        const float pv = pw[k].get(e);
-        tgt += mass_of(pv);
-        if (!bonus) res += residual_of(pv, qw[k].get(e));
+      for (int k = 0; k < kAhead; ++k) {
+        const int v = t + k < t1 ? (t + k) * kTile + lane * kEach : V;  // V: nothing, zeros
+        pe[k].load(P, v, V, wide_p);
+        if (kRes) qe[k].load(Q, v, V, wide_q);
       }
-  }
+    };
+    double sum[2] = {0.0, 0.0};
+    if (t0 < t1) fetch(t0, pw, qw);
+    for (int t = t0; t < t1; t += kAhead) {
+      if (t + kAhead < t1) fetch(t + kAhead, pn, qn);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    res += __shfl_xor_sync(0xffffffffu, res, o);
-    tgt += __shfl_xor_sync(0xffffffffu, tgt, o);
-  }
-  if (C > 1) {
-    cg::cluster_group cl = cg::this_cluster();
-    cl.barrier_wait();
-    if (lane < C) cl.map_shared_rank(chunk, lane)[mine] = make_double2(res, tgt);
-    cl.sync();
-  } else {
-    if (lane == 0) chunk[mine] = make_double2(res, tgt);
-    __syncthreads();
-  }
-
-  // every warp alike: the totals, and the first chunk that passes the draw (else
+      for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+        for (int e = 0; e < kEach; ++e)
+          add_mass<kRes>(sum[k], pw[k].get(e), kRes ? qw[k].get(e) : 0.f);
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        pw[k] = pn[k];
+        qw[k] = qn[k];
+      }
+    }
+    double all = sum[0] + sum[1];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    return all;
+  };
+  // the chunk sums of the whole row in every CTA; round 1 only where a residual
+  // has no mass at all
+  auto share = [&](double mass, int round) {
+    if (C > 1) {
+      cg::cluster_group cl = cg::this_cluster();
+      if (round == 0) cl.barrier_wait();
+      if (lane < C) cl.map_shared_rank(&chunk[round][0], lane)[mine] = mass;
+      cl.sync();
+    } else {
+      if (lane == 0) chunk[round][mine] = mass;
+      __syncthreads();
+    }
+  };
+  bool from_res = !bonus;
+  int round = 0;
+  share(bonus ? sum_chunk(std::false_type()) : sum_chunk(std::true_type()), 0);
+  // Every warp alike: the total, and the first chunk that passes the draw (else
   // the last one with mass).  Lane l holds chunks 2 l and 2 l + 1.
-  double2 c0 = make_double2(0.0, 0.0), c1 = c0;
-  if (2 * lane < chunks) c0 = chunk[2 * lane];
-  if (2 * lane + 1 < chunks) c1 = chunk[2 * lane + 1];
-  const bool from_res = !bonus && __any_sync(0xffffffffu, c0.x > 0.0 || c1.x > 0.0);
-  const double m0 = from_res ? c0.x : c0.y, m1 = from_res ? c1.x : c1.y;
+  double m0, m1;
+  auto look = [&]() {
+    m0 = 2 * lane < chunks ? chunk[round][2 * lane] : 0.0;
+    m1 = 2 * lane + 1 < chunks ? chunk[round][2 * lane + 1] : 0.0;
+    return __any_sync(0xffffffffu, m0 > 0.0 || m1 > 0.0);
+  };
+  if (!look() && from_res) {
+    from_res = false;
+    round = 1;
+    share(sum_chunk(std::false_type()), 1);
+    look();
+  }
   const double pre = warp_prefix(m0 + m1), total = __shfl_sync(0xffffffffu, pre, 31);
   const double goal = fmax((double)u_draw, 0.0) * total;
   const double up = __shfl_up_sync(0xffffffffu, pre, 1);
@@ -246,7 +277,11 @@ __global__ void __launch_bounds__(kThreads)
     double m[kEach], sum = 0.0;
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
-      m[e] = from_res ? residual_of(pw.get(e), qw.get(e)) : mass_of(pw.get(e));
+      m[e] = 0.0;
+      if (from_res)
+        add_mass<true>(m[e], pw.get(e), qw.get(e));
+      else
+        add_mass<false>(m[e], pw.get(e), 0.f);
       sum += m[e];
     }
     const double incl = warp_prefix(sum);

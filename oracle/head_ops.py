@@ -162,7 +162,8 @@ def verify_probs(target, draft_probs, draft, u_accept, u_draw, verify_len=None):
         m = mass(target[b, j])
         if j < kb:
             with np.errstate(invalid="ignore"):
-                res = mass(m - np.asarray(draft_probs[b, j], np.float64)) * (m > 0)
+                q = np.asarray(draft_probs[b, j], np.float64)
+                res = np.maximum(m - np.where(q > 0, q, 0.0), 0.0)
             if res.sum() > 0:
                 m = res
         cum = np.cumsum(m)
