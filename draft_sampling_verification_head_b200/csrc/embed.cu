@@ -106,20 +106,50 @@ SPEC_DEV void store8(T* p, const Columns<kWide>& c, const float* x) {
   }
 }
 
-// rows[i] = scale * table[ids[i]]: one CTA per row.
-template <typename TT, typename TR>
-__global__ void __launch_bounds__(kThreads)
+// rows[i] = scale * table[ids[i]].  `lanes` lanes take one row of four blocks of
+// columns at a time, or kRows rows of 4 / kRows blocks, so that four blocks' loads
+// are in flight together (single columns, which cost eight loads a block, take one
+// block of each row).  Bytes bound it: the named rows of the table in, the rows out.
+template <bool kWide, int kRows, typename TT, typename TR>
+__global__ void __launch_bounds__(kThreads, kWide ? 1 : 4)
     k_embed(spec_embed_params p, const TT* __restrict__ table, const int32_t* __restrict__ ids,
-            TR* __restrict__ rows, WsHeader* hdr) {
-  const int i = blockIdx.x;
-  const int id = ids[i];
-  const bool in = id >= 0 && id < p.V;
-  if (!in && id != -1 && threadIdx.x == 0)
-    report_error(hdr, SPEC_ERR_TOKEN_RANGE, SITE_TOKEN_RANGE, i, id);
-  const TT* src = table + (int64_t)(in ? id : 0) * p.table_stride;
-  TR* dst = rows + (int64_t)i * p.row_stride;
-  for (int c = threadIdx.x; c < p.D; c += kThreads)
-    store_f(dst, c, in ? load_f(src, c) * p.scale : 0.f);
+            TR* __restrict__ rows, int shift, WsHeader* hdr) {
+  constexpr int kAhead = kWide ? 4 : kRows, kBlocks = kAhead / kRows;
+  const int lanes = 1 << shift, lane = threadIdx.x & (lanes - 1);
+  const int64_t i0 = (((int64_t)blockIdx.x * kThreads + threadIdx.x) >> shift) * kRows;
+  int id[kRows];
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) id[r] = i0 + r < p.n ? __ldg(ids + i0 + r) : -1;
+  bool in[kRows];
+  const TT* src[kRows];
+  TR* dst[kRows];
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    in[r] = id[r] >= 0 && id[r] < p.V;
+    src[r] = table + (int64_t)(in[r] ? id[r] : 0) * p.table_stride;
+    dst[r] = rows + (i0 + r) * p.row_stride;
+    if (!in[r] && id[r] != -1 && lane == 0)
+      report_error(hdr, SPEC_ERR_TOKEN_RANGE, SITE_TOKEN_RANGE, (int)(i0 + r), id[r]);
+  }
+  const int blocks = (p.D + kCols * lanes - 1) / (kCols * lanes);
+  for (int k0 = 0; k0 < blocks; k0 += kBlocks) {
+    Raw<kWide, TT> x[kAhead];
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) {
+      const int r = q / kBlocks;
+      const Columns<kWide> c(k0 + q % kBlocks, lane, lanes, p.D);  // none past the last block
+      x[q].load(src[r] + c.at, c);
+    }
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) {
+      const int r = q / kBlocks;
+      const Columns<kWide> c(k0 + q % kBlocks, lane, lanes, p.D);
+      float y[kCols];
+#pragma unroll
+      for (int k = 0; k < kCols; ++k) y[k] = in[r] ? x[q].get(k) * p.scale : 0.f;
+      if (c.any() && i0 + r < p.n) store8<kWide>(dst[r] + c.at, c, y);
+    }
+  }
 }
 
 // ----------------------------------------------------------------------------
@@ -715,20 +745,33 @@ size_t embed_grad_ws_bytes(const spec_embed_params& p) {
   return p.n <= kDirect ? 0 : plan_of(p).bytes;
 }
 
-template <typename TT, typename TR>
-cudaError_t launch_embed(const spec_embed_params& p, const TT* table, const int32_t* ids, TR* rows,
-                         WsHeader* hdr, int, cudaStream_t st, int* launches) {
-  k_embed<TT, TR><<<p.n, kThreads, 0, st>>>(p, table, ids, rows, hdr);
-  *launches = 1;
-  return cudaGetLastError();
-}
-
-// Rows of whole 16-byte vectors of both tensors.
+// Rows of whole vectors of four columns, 16-byte aligned, in both tensors.
 template <typename TT, typename TR>
 bool wide_ok(const spec_embed_params& p, const void* table, const void* rows) {
   return p.D % 4 == 0 && p.table_stride * sizeof(TT) % 16 == 0 &&
          p.row_stride * sizeof(TR) % 16 == 0 &&
          ((reinterpret_cast<uintptr_t>(table) | reinterpret_cast<uintptr_t>(rows)) & 15) == 0;
+}
+
+template <typename TT, typename TR>
+cudaError_t launch_embed(const spec_embed_params& p, const TT* table, const int32_t* ids, TR* rows,
+                         WsHeader* hdr, int, cudaStream_t st, int* launches) {
+  int shift = 0;  // log2 of the lanes per row
+  while (shift < 5 && (kCols << shift) < p.D) ++shift;
+  const int blocks = (p.D + (kCols << shift) - 1) / (kCols << shift);
+  const int per = blocks == 1 ? 4 : blocks == 2 ? 2 : 1;  // rows that lanes take together
+  const int64_t groups = ((int64_t)p.n + per - 1) / per;
+  const int64_t grid = ((groups << shift) + kThreads - 1) / kThreads;
+  if (grid > INT32_MAX) return cudaErrorInvalidValue;
+  *launches = 1;
+  const bool wide = wide_ok<TT, TR>(p, table, rows);
+  auto run = [&](auto kernel) {
+    kernel<<<(unsigned)grid, kThreads, 0, st>>>(p, table, ids, rows, shift, hdr);
+    return cudaGetLastError();
+  };
+  if (per == 4) return wide ? run(k_embed<true, 4, TT, TR>) : run(k_embed<false, 4, TT, TR>);
+  if (per == 2) return wide ? run(k_embed<true, 2, TT, TR>) : run(k_embed<false, 2, TT, TR>);
+  return wide ? run(k_embed<true, 1, TT, TR>) : run(k_embed<false, 1, TT, TR>);
 }
 
 template <typename TT, typename TR>
