@@ -7,6 +7,7 @@
 #include <cstring>
 
 #include "common.cuh"
+#include "head_ops.cuh"
 #include "kernels.cuh"
 #include "specdec_debug.h"
 

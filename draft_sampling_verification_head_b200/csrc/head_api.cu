@@ -5,7 +5,6 @@
 #include <cstdio>
 
 #include "head_ops.cuh"
-#include "kernels.cuh"
 
 namespace specdec {
 namespace {

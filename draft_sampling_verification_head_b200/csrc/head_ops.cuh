@@ -6,6 +6,10 @@
 
 namespace specdec {
 
+// ---- Shared by the entry points (api.cu) ------------------------------------------
+extern thread_local int32_t g_last_launches;  // kernel launches of the thread's last call
+int num_sms();                                // SMs of the current device, 0 on an error
+
 // Record a device-side error of an operator: the first one stays.  Unlike
 // record_error this leaves the abort flag alone, which only the persistent
 // kernels of the cycle poll and reset.

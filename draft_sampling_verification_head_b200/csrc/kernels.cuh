@@ -20,10 +20,6 @@ struct StopInfo {
   float sz;
 };
 
-// ---- Shared by the entry points ----------------------------------------------
-extern thread_local int32_t g_last_launches;  // kernel launches of the thread's last call
-int num_sms();                                // SMs of the current device, 0 on an error
-
 // ---- Markov bias, one step -------------------------------------------------
 size_t bias_tc_smem_bytes(int r, int N);
 cudaError_t launch_bias_tc(const CUtensorMap& tmW, const __nv_bfloat16* U, const int32_t* prev,
