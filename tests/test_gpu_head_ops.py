@@ -349,7 +349,10 @@ def test_scan_no_steps_and_bad_lengths():
 # ---------------------------------------------------------------------------
 W4 = [(1, 32, 1, 32), (1, 64, 17, 64), (2, 128, 100, 128), (3, 96, 1000, 32), (1, 256, 5003, 32),
       (7, 320, 129, 64), (16, 384, 2000, 128), (17, 256, 333, 64), (33, 128, 70, 32),
-      (5, 4096, 300, 128), (16, 2080, 65, 32), (8, 1024, 4096, 64)]
+      (5, 4096, 300, 128), (16, 2080, 65, 32), (8, 1024, 4096, 64),
+      # vocabularies that fill the GPU
+      (1, 32, 9472, 32), (1, 256, 9999, 32), (16, 384, 20001, 128), (3, 96, 40010, 32), (17, 320, 9601, 64),
+      (9, 640, 12345, 128), (10, 64, 30000, 64), (33, 128, 19000, 32)]
 
 
 def w4_inputs(B, r, V, group, dtype, sdtype, g):
