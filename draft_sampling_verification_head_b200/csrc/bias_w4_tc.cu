@@ -7,10 +7,10 @@
 // needs: one, or three whose sum is an fp32 exactly) is the B operand in shared
 // memory.  The MMA of a group of features adds into an accumulator of its own;
 // the thread reads it back, scales it in fp32 and adds it to its token's sums in
-// registers, so no scaled weight is ever rounded.  While one half block is
-// multiplied the quartet unpacks the next: two A buffers, two accumulators.
+// registers, so no scaled weight is ever rounded.  A warp of its own issues the
+// quartet's MMAs; while they run the quartet unpacks the next half blocks.
 //
-// A CTA per SM runs up to four quartets on tiles of their own in step, so that a
+// A CTA per SM runs up to three quartets on tiles of their own in step, so that a
 // block of X, which one warp copies through a ring, serves all of them.  Codes go
 // through rings of 16-byte asynchronous copies, private to a warp.  Tiles are cut
 // to equal numbers of tokens so that every SM gets as many.
@@ -29,19 +29,23 @@ constexpr uint64_t kPolls = 1ull << 22;
 
 template <int NC, int G>
 struct Plan {
-  static constexpr int kPer = 128 / G;                       // groups per block
-  static constexpr int kDBufs = G == 32 ? 4 : 2;             // accumulators per quartet
-  static constexpr int kCols = 2 * kACols + kDBufs * NC;     // tensor memory per quartet
+  static constexpr int kPer = 128 / G;  // groups per block
+  // half blocks between a store of A and the reading of its products, as many as
+  // tensor memory allows: an MMA's way there and back takes longer than a half block
+  static constexpr int kLag = NC > 16 && G == 32 ? 1 : 2;
+  static constexpr int kA = kLag + 1;   // A buffers
+  static constexpr int kDBufs = G == 128 ? 2 : G == 64 ? kA : 2 * kA;  // accumulators
+  static constexpr int kCols = kA * kACols + kDBufs * NC;  // tensor memory per quartet
   // quartets that tensor memory and the register file hold
-  static constexpr int kMaxQ = NC == 16 ? 4 : (NC == 32 ? (G == 32 ? 2 : 3) : (G == 32 ? 2 : 3));
-  static constexpr int kBBytes = NC * 256;                   // a block of X
-  static constexpr int kThreadsMax = kMaxQ * 128 + 32;
-  static_assert(kMaxQ * kCols <= 512, "tensor memory");
+  static constexpr int kMaxQ = 512 / kCols < 3 ? 512 / kCols : 3;
+  static constexpr int kBBytes = NC * 256;  // a block of X
+  static constexpr int kThreadsMax = kMaxQ * 160 + 32;
+  static_assert(kMaxQ >= 2, "tensor memory");
 };
 
 struct Ctl {
   uint64_t bfull[kBStages], bempty[kBStages];
-  uint64_t dfull[4][2];
+  uint64_t aready[4][3], dfull[4][3];
   uint32_t tmem;
   uint32_t failed;
 };
@@ -111,7 +115,7 @@ SPEC_DEV void wait_for(uint64_t* bar, uint32_t parity, Ctl* ctl, WsHeader* hdr, 
   report_error(hdr, SPEC_ERR_TIMEOUT, site, blockIdx.x, 0);
 }
 
-template <int NC, int G>
+template <typename TS, int NC, int G>
 __global__ void __launch_bounds__(Plan<NC, G>::kThreadsMax, 1) k_bias_w4_tc(Args a) {
   using P = Plan<NC, G>;
   extern __shared__ uint8_t smem_raw[];
@@ -127,7 +131,10 @@ __global__ void __launch_bounds__(Plan<NC, G>::kThreadsMax, 1) k_bias_w4_tc(Args
       mbar_init(&ctl->bempty[i], Q);
     }
     for (int q = 0; q < 4; ++q)
-      for (int i = 0; i < 2; ++i) mbar_init(&ctl->dfull[q][i], 1);
+      for (int i = 0; i < P::kA; ++i) {
+        mbar_init(&ctl->aready[q][i], 4);
+        mbar_init(&ctl->dfull[q][i], 1);
+      }
     ctl->failed = 0;
     fence_mbar_init();
   }
@@ -140,99 +147,149 @@ __global__ void __launch_bounds__(Plan<NC, G>::kThreadsMax, 1) k_bias_w4_tc(Args
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
 
-  if (warp == 4 * Q) {
+  // accumulator of group j of half block s (all groups of 128: of its block), as
+  // a column of the quartet's
+  auto d_at = [&](int s, int j) {
+    const int buf = G == 128 ? (s >> 1) & 1 : G == 64 ? s % P::kA : (s % P::kA) * 2 + j;
+    return P::kA * kACols + buf * NC;
+  };
+
+  if (warp == 5 * Q) {
     // ---- blocks of X through the ring ----
     if (lane == 0) {
       grid_dependency_wait();
       const uint8_t* src = a.xf + (int64_t)blockIdx.y * nkb * P::kBBytes;
       const uint64_t policy = policy_evict_last();
-      for (int it = 0; it < steps; ++it) {
+      for (int it = 0, kb = 0; it < steps; ++it) {
         const int slot = it % kBStages;
         if (it >= kBStages)
           wait_for(&ctl->bempty[slot], (it / kBStages - 1) & 1, ctl, a.hdr, SITE_MBAR_BASE);
         if (ld_volatile_u32(&ctl->failed)) break;
         mbar_arrive_expect_tx(&ctl->bfull[slot], P::kBBytes);
-        bulk_load(sB + slot * P::kBBytes, src + (int64_t)(it % nkb) * P::kBBytes, P::kBBytes,
+        bulk_load(sB + slot * P::kBBytes, src + (int64_t)kb * P::kBBytes, P::kBBytes,
                   &ctl->bfull[slot], policy);
+        if (++kb == nkb) kb = 0;
       }
       // the last blocks' commits land before the CTA may end
       for (int it = max(steps - kBStages, 0); it < steps; ++it)
         wait_for(&ctl->bempty[it % kBStages], (it / kBStages) & 1, ctl, a.hdr, SITE_MBAR_BASE);
     }
     __syncwarp();
-  } else if (warp < 4 * Q) {
+  } else if (warp >= 4 * Q) {
+    // ---- a quartet's matrix instructions, by one thread ----
+    if (lane == 0) {
+      const int q = warp - 4 * Q;
+      const uint32_t tq = tmem + q * P::kCols;
+      const uint32_t idesc = idesc_bf16_f32(128, NC, false, false);
+      uint32_t buf = 0, par = 0;  // s % kA, (s / kA) & 1
+      for (int s = 0; s < 2 * steps; ++s) {
+        const int it = s >> 1, slot = it % kBStages;
+        wait_for(&ctl->aready[q][buf], par, ctl, a.hdr, SITE_MBAR_BREADY);
+        if ((s & 1) == 0) wait_for(&ctl->bfull[slot], (it / kBStages) & 1, ctl, a.hdr, SITE_MBAR_FULL);
+        tc_fence_after();
+        const uint32_t b0 = smem_u32(sB + slot * P::kBBytes + (s & 1) * (NC * 128));
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+          const int g = G == 32 ? ks >> 1 : 0;
+          const bool first = G == 32 ? (ks & 1) == 0 : G == 64 ? ks == 0 : ((s & 1) == 0 && ks == 0);
+          umma_ts(tq + d_at(s, g), tq + buf * kACols + ks * 8, smem_desc_sw128(b0 + ks * 32, 16, 1024),
+                  idesc, first ? 0u : 1u);
+        }
+        umma_commit(&ctl->dfull[q][buf]);
+        if (s & 1) umma_commit(&ctl->bempty[slot]);
+        if (++buf == P::kA) {
+          buf = 0;
+          par ^= 1;
+        }
+      }
+    }
+    __syncwarp();
+  } else {
     const int q = warp >> 2, w4 = warp & 3, m = w4 * 32 + lane;  // the thread's token of the tile
     uint8_t* ring = sC + (size_t)warp * kCStages * kCodeBytes;
     const int rowb = nkb * 64, ng = a.p.r / G;
-    const bool bf16_scales = a.p.scale_dtype == SPEC_BF16;
     const int64_t cta0 = (int64_t)blockIdx.x * a.rounds * Q * a.tokens;
     auto tile_at = [&](int round) { return cta0 + (int64_t)(round * Q + q) * a.tokens; };
     // token m of a tile exists
     auto token_in = [&](int64_t v0, int k) { return k < a.tokens && v0 + k < V; };
 
     // the warp's 32 rows of a block: eight rows of 64 bytes per instruction,
-    // swizzled so that a thread's later 16-byte reads of its row hit all banks
-    auto request = [&](int it) {
-      if (it < steps) {
-        const int64_t v0 = tile_at(it / nkb);
-        const int kb = it % nkb, c = lane & 3;
-        uint8_t* to = ring + (it % kCStages) * kCodeBytes;
+    // swizzled so that a thread's later 16-byte reads of its row hit all banks.
+    // Blocks are asked for in order, so places advance by addition.
+    int r_round = 0, r_kb = 0, r_slot = 0;
+    const uint8_t* r_src = nullptr;
+    bool r_in[4];
+    const uint32_t r_to = smem_u32(ring) + (lane >> 3) * 128 +
+                          (((lane >> 2) & 1) * 4 + ((lane & 3) ^ ((lane >> 3) & 3))) * 16;
+    const int64_t row8 = (int64_t)8 * rowb;
+    auto request = [&]() {
+      if (r_round < a.rounds) {
+        if (r_kb == 0) {
+          const int64_t v0 = tile_at(r_round);
+          const int r = w4 * 32 + (lane >> 2);
+          r_src = a.wq + (v0 + r) * rowb + (lane & 3) * 16;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int r = (lane >> 2) + 8 * j;
-          const bool in = token_in(v0, w4 * 32 + r);
-          const uint8_t* src = in ? a.wq + (v0 + w4 * 32 + r) * rowb + kb * 64 + c * 16 : a.wq;
+          for (int j = 0; j < 4; ++j) r_in[j] = token_in(v0, r + 8 * j);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {  // row + 8 j: four lines of 128 bytes further
+          const uint8_t* src = r_in[j] ? r_src + j * row8 : a.wq;
           asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(
-                           smem_u32(to + (r >> 1) * 128 + ((r & 1) * 4 + (c ^ ((r >> 1) & 3))) * 16)),
-                       "l"(src), "r"(in ? 16 : 0)
+                           r_to + r_slot * kCodeBytes + j * 512),
+                       "l"(src), "r"(r_in[j] ? 16 : 0)
                        : "memory");
+        }
+        r_src += 64;
+        if (++r_slot == kCStages) r_slot = 0;
+        if (++r_kb == nkb) {
+          r_kb = 0;
+          ++r_round;
         }
       }
       cp_async_commit();
     };
-    // the token's scales of a block, as they lie in memory
-    auto scales = [&](int it, uint32_t (&s)[P::kPer]) {
+    // the token's scales of the next block, as they lie in memory: loads without
+    // a condition (rows and groups that do not exist read ones that do, and scale
+    // zeros), so that nothing waits for them before they are used
+    int c_round = 0, c_kb = 0;
+    const TS* c_src = nullptr;
+    auto scales = [&](TS (&s)[P::kPer]) {
+      if (c_kb == 0)
+        c_src = (const TS*)a.wscale + min(tile_at(min(c_round, a.rounds - 1)) + m, (int64_t)V - 1) * ng;
 #pragma unroll
-      for (int j = 0; j < P::kPer; ++j) s[j] = 0u;
-      if (it >= steps) return;
-      const int64_t v0 = tile_at(it / nkb);
-      if (!token_in(v0, m)) return;
-      const int64_t at = (v0 + m) * ng;
-#pragma unroll
-      for (int j = 0; j < P::kPer; ++j) {
-        const int g = min((it % nkb) * P::kPer + j, ng - 1);
-        s[j] = bf16_scales ? (uint32_t)__ldg((const unsigned short*)a.wscale + at + g)
-                           : __ldg((const uint32_t*)a.wscale + at + g);
+      for (int j = 0; j < P::kPer; ++j) s[j] = c_src[min(c_kb * P::kPer + j, ng - 1)];
+      if (++c_kb == nkb) {
+        c_kb = 0;
+        ++c_round;
       }
     };
 
-    const uint32_t tq = tmem + q * P::kCols;                      // the quartet's columns
-    const uint32_t lanes = (uint32_t)(w4 * 32) << 16;
-    const uint32_t idesc = idesc_bf16_f32(128, NC, false, false);
-    // accumulator of group j of half block s (all groups of 128: of its block)
-    auto d_at = [&](int s, int j) {
-      const int buf = G == 128 ? (s >> 1) & 1 : G == 64 ? s & 1 : (s & 1) * 2 + j;
-      return tq + 2 * kACols + buf * NC;
-    };
+    const uint32_t tq = tmem + q * P::kCols + ((uint32_t)(w4 * 32) << 16);  // its columns, own lanes
     float total[NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) total[c] = 0.f;
 
-    // adds what half block s (of block it) accumulated, if a group ends with it
-    auto gather = [&](int s, const uint32_t (&sc)[P::kPer]) {
-      wait_for(&ctl->dfull[q][s & 1], (s >> 1) & 1, ctl, a.hdr, SITE_MBAR_MMA);
+    // adds what half block s accumulated, if a group ends with it; half blocks are
+    // gathered in order
+    uint32_t g_buf = 0, g_par = 0;
+    auto gather = [&](int s, int half, const TS (&sc)[P::kPer]) {
+      wait_for(&ctl->dfull[q][g_buf], g_par, ctl, a.hdr, SITE_MBAR_MMA);
+      if (++g_buf == P::kA) {
+        g_buf = 0;
+        g_par ^= 1;
+      }
       tc_fence_after();
-      if (G == 128 && (s & 1) == 0) return;
+      if (G == 128 && half == 0) return;
       constexpr int kGroups = G == 32 ? 2 : 1;
 #pragma unroll
       for (int j = 0; j < kGroups; ++j) {
-        const uint32_t raw = G == 32 ? ((s & 1) ? sc[(2 + j) % P::kPer] : sc[j % P::kPer])
-                             : G == 64 ? ((s & 1) ? sc[1 % P::kPer] : sc[0]) : sc[0];
-        const float scale = __uint_as_float(bf16_scales ? raw << 16 : raw);
+        const TS raw = G == 32 ? (half ? sc[(2 + j) % P::kPer] : sc[j % P::kPer])
+                       : G == 64 ? (half ? sc[1 % P::kPer] : sc[0]) : sc[0];
+        const float scale = (float)raw;
 #pragma unroll
         for (int c = 0; c < NC; c += 16) {
           float d[16];
-          tmem_ld16(d_at(s, j) + lanes + c, d);
+          tmem_ld16(tq + d_at(s, j) + c, d);
           tmem_ld_wait();
 #pragma unroll
           for (int k = 0; k < 16; ++k) total[c + k] = fmaf(scale, d[k], total[c + k]);
@@ -275,12 +332,15 @@ __global__ void __launch_bounds__(Plan<NC, G>::kThreadsMax, 1) k_bias_w4_tc(Args
     };
 
 #pragma unroll
-    for (int k = 0; k < kCStages - 1; ++k) request(k);
-    uint32_t s_old[P::kPer], s_now[P::kPer], s_next[P::kPer];
-    scales(0, s_next);
-#pragma unroll
-    for (int j = 0; j < P::kPer; ++j) s_now[j] = 0u;
-    for (int it = 0; it < steps; ++it) {
+    for (int k = 0; k < kCStages - 1; ++k) request();
+    // Two sets of scales, of even and of odd blocks; a set is asked for again as
+    // soon as its block's last group has been gathered, a block before its next
+    // use, and no copy of it in between waits for it.
+    TS sc[2][P::kPer];
+    scales(sc[0]);
+    int round = 0, kb = 0;
+    uint32_t a_buf = 0;  // half block % kA
+    auto block = [&](int it, TS (&s_now)[P::kPer], TS (&s_other)[P::kPer]) {
       cp_async_wait<kCStages - 2>();
       __syncwarp();
       uint4 w[4];  // chunk t: word t of each 32 features
@@ -291,13 +351,7 @@ __global__ void __launch_bounds__(Plan<NC, G>::kThreadsMax, 1) k_bias_w4_tc(Args
           w[t] = *reinterpret_cast<const uint4*>(from + ((lane & 1) * 4 + (t ^ ((lane >> 1) & 3))) * 16);
       }
       __syncwarp();
-      request(it + kCStages - 1);
-#pragma unroll
-      for (int j = 0; j < P::kPer; ++j) {
-        s_old[j] = s_now[j];
-        s_now[j] = s_next[j];
-      }
-      scales(it + 1, s_next);
+      request();
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int s = 2 * it + h;
@@ -310,37 +364,42 @@ __global__ void __launch_bounds__(Plan<NC, G>::kThreadsMax, 1) k_bias_w4_tc(Args
 #pragma unroll
             for (int k = 0; k < 4; ++k) pk[4 * j + k] = pair[k];
           }
-          tmem_store32(tq + lanes + h * kACols, pk);
+          tmem_store32(tq + a_buf * kACols, pk);
           tmem_st_wait();
         }
         tc_fence_before();
-        asm volatile("bar.sync %0, 128;" ::"r"(1 + q) : "memory");
-        if (w4 == 0 && lane == 0) {
-          tc_fence_after();
-          const int slot = it % kBStages;
-          if (h == 0) wait_for(&ctl->bfull[slot], (it / kBStages) & 1, ctl, a.hdr, SITE_MBAR_FULL);
-          const uint32_t b0 = smem_u32(sB + slot * P::kBBytes + h * (NC * 128));
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks) {
-            const int g = G == 32 ? ks >> 1 : 0;
-            const bool first = G == 32 ? (ks & 1) == 0 : G == 64 ? ks == 0 : (h == 0 && ks == 0);
-            umma_ts(d_at(s, g), tq + h * kACols + ks * 8, smem_desc_sw128(b0 + ks * 32, 16, 1024),
-                    idesc, first ? 0u : 1u);
-          }
-          umma_commit(&ctl->dfull[q][h]);
-          if (h == 1) umma_commit(&ctl->bempty[slot]);
-        }
         __syncwarp();
-        if (s > 0) {
-          if (h == 0)
-            gather(s - 1, s_old);
-          else
-            gather(s - 1, s_now);
-          if (h == 0 && it % nkb == 0) put(it / nkb - 1);  // the tile before is whole
+        if (lane == 0) mbar_arrive(&ctl->aready[q][a_buf]);
+        if (++a_buf == P::kA) a_buf = 0;
+        // what lies kLag half blocks back; this store's buffer comes free with it
+        if constexpr (P::kLag == 1) {
+          if (h == 1) {
+            gather(s - 1, 0, s_now);
+          } else {
+            if (it > 0) gather(s - 1, 1, s_other);
+            if (kb == 0 && it > 0) put(round - 1);  // the tile before is whole
+            scales(s_other);
+          }
+        } else {
+          if (it > 0) gather(s - 2, h, s_other);
+          if (h == 1) {
+            if (kb == 0 && it > 0) put(round - 1);
+            scales(s_other);
+          }
         }
       }
+      if (++kb == nkb) {
+        kb = 0;
+        ++round;
+      }
+    };
+    for (int it = 0; it < steps; it += 2) {
+      block(it, sc[0], sc[1]);
+      if (it + 1 < steps) block(it + 1, sc[1], sc[0]);
     }
-    gather(2 * steps - 1, s_now);
+    TS(&s_last)[P::kPer] = sc[(steps & 1) ? 0 : 1];
+    if constexpr (P::kLag == 2) gather(2 * steps - 2, 0, s_last);
+    gather(2 * steps - 1, 1, s_last);
     put(a.rounds - 1);
     tc_fence_before();
   }
@@ -361,7 +420,7 @@ int rows_of(const spec_w4_params& p, int NC) {
   return std::min(p.dtype == SPEC_BF16 ? NC : NC / 3, 16);
 }
 
-template <int NC, int G>
+template <typename TS, int NC, int G>
 cudaError_t product(Args& a, int num_sms, cudaStream_t st) {
   using P = Plan<NC, G>;
   // as many quartets as fit, and tiles as full as an equal share per SM allows
@@ -383,10 +442,26 @@ cudaError_t product(Args& a, int num_sms, cudaStream_t st) {
   const size_t smem = 1024 + kBStages * P::kBBytes +
                       (size_t)a.quartets * 4 * kCStages * kCodeBytes + sizeof(Ctl);
   const cudaError_t e = cudaFuncSetAttribute(
-      k_bias_w4_tc<NC, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      k_bias_w4_tc<TS, NC, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_after(k_bias_w4_tc<NC, G>, dim3(grid, (a.p.B + a.rows - 1) / a.rows),
-                      a.quartets * 128 + 32, smem, st, a);
+  return launch_after(k_bias_w4_tc<TS, NC, G>, dim3(grid, (a.p.B + a.rows - 1) / a.rows),
+                      a.quartets * 160 + 32, smem, st, a);
+}
+
+template <typename TS>
+cudaError_t by_shape(Args& a, int NC, int num_sms, cudaStream_t st) {
+  const int G = a.p.group;
+  if (NC == 16)
+    return G == 32   ? product<TS, 16, 32>(a, num_sms, st)
+           : G == 64 ? product<TS, 16, 64>(a, num_sms, st)
+                     : product<TS, 16, 128>(a, num_sms, st);
+  if (NC == 32)
+    return G == 32   ? product<TS, 32, 32>(a, num_sms, st)
+           : G == 64 ? product<TS, 32, 64>(a, num_sms, st)
+                     : product<TS, 32, 128>(a, num_sms, st);
+  return G == 32   ? product<TS, 48, 32>(a, num_sms, st)
+         : G == 64 ? product<TS, 48, 64>(a, num_sms, st)
+                   : product<TS, 48, 128>(a, num_sms, st);
 }
 
 }  // namespace
@@ -421,17 +496,8 @@ cudaError_t launch_bias_w4_tc(const spec_w4_params& p, const T* x, const int32_t
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   *launches = 2;
-  if (NC == 16)
-    return p.group == 32   ? product<16, 32>(a, num_sms, st)
-           : p.group == 64 ? product<16, 64>(a, num_sms, st)
-                           : product<16, 128>(a, num_sms, st);
-  if (NC == 32)
-    return p.group == 32   ? product<32, 32>(a, num_sms, st)
-           : p.group == 64 ? product<32, 64>(a, num_sms, st)
-                           : product<32, 128>(a, num_sms, st);
-  return p.group == 32   ? product<48, 32>(a, num_sms, st)
-         : p.group == 64 ? product<48, 64>(a, num_sms, st)
-                         : product<48, 128>(a, num_sms, st);
+  return p.scale_dtype == SPEC_BF16 ? by_shape<__nv_bfloat16>(a, NC, num_sms, st)
+                                    : by_shape<float>(a, NC, num_sms, st);
 }
 
 #define SPEC_INST(T)                                                                               \
