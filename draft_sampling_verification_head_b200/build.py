@@ -12,7 +12,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libspecdec.so")
 SOURCES = ["api.cu", "bias_gemm.cu", "verify.cu", "verify_ee.cu", "cycle.cu", "cycle_tc.cu",
            "noalloc.cu", "schedule.cpp", "head_api.cu", "embed.cu", "scan.cu", "bias_w4.cu",
-           "bias_w4_tc.cu", "verify_probs.cu"]
+           "verify_probs.cu"]
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "--threads", "4", "-Xptxas", "-v"]
 
