@@ -161,15 +161,15 @@ _DT = {"f32": SPEC_F32, "bf16": SPEC_BF16}
 class _Held:
     """What a parameter object's calls need again and again, made once: the
     objects are frozen.  _c is the C structure, _at its address, _need the
-    workspace size and _args, by call, (name, dtype, least number of elements
-    reachable from the first one) of each tensor."""
+    workspace size and _args, by call, (name, dtype, rows, row stride, row
+    width) of each tensor, which _ready holds as the call looks at them."""
 
     def __getattr__(self, name):
-        if name not in ("_c", "_at", "_need", "_args"):
+        if name not in ("_c", "_at", "_need", "_args", "_ready"):
             raise AttributeError(name)
         c = self._make()
         for k, v in (("_c", c), ("_at", ctypes.addressof(c)), ("_args", self._tensors()),
-                     ("_need", SPEC_WORKSPACE_MIN)):
+                     ("_ready", {}), ("_need", SPEC_WORKSPACE_MIN)):
             object.__setattr__(self, k, v)
         if isinstance(self, EmbedParams):
             object.__setattr__(self, "_need", int(lib().spec_embed_workspace_size(self._at)))
@@ -184,11 +184,6 @@ class _Held:
 
     def __reduce__(self):  # copies make their own C structure
         return type(self), tuple(getattr(self, f.name) for f in fields(self))
-
-
-def _span(rows, stride, width):
-    """Elements from the first to the last of `rows` rows, `stride` (0: dense) apart."""
-    return 0 if rows <= 0 else (rows - 1) * (stride or width) + width
 
 
 @dataclass(frozen=True)
@@ -210,9 +205,9 @@ class EmbedParams(_Held):
                                self.table_stride, self.row_stride)
 
     def _tensors(self):
-        table = (self.dtype, _span(self.V, self.table_stride, self.D))
-        rows = (self.row_dtype, _span(self.n, self.row_stride, self.D))
-        ids = ("ids", "i32", self.n)
+        table = (self.dtype, self.V, self.table_stride or self.D, self.D)
+        rows = (self.row_dtype, self.n, self.row_stride or self.D, self.D)
+        ids = ("ids", "i32", 1, self.n, self.n)
         return {"embed": (("table", *table), ids, ("rows", *rows)),
                 "embed_grad": (ids, ("drows", *rows), ("dtable", *table))}
 
@@ -233,17 +228,18 @@ class ScanParams(_Held):
                               self.x_stride, self.h_stride)
 
     def _tensors(self):
-        n, e = self.B * self.T, self.B * self.D
-        gate = (self.dtype, _span(n, self.gate_stride, self.D))
-        x = (self.dtype, _span(n, self.x_stride, self.D))
-        h = (self.dtype, _span(n, self.h_stride, self.D))
-        lens = ("len", "i32", self.B)
-        states = ("states", "f32", -(-self.T // SPEC_SCAN_CHUNK) * e)
-        return {"scan": (("gate", *gate), ("x", *x), ("h0", "f32", e), lens, ("h", *h),
-                         ("h_last", "f32", e), states),
-                "scan_grad": (("gate", *gate), ("x", *x), ("h0", "f32", e), lens, states,
-                              ("dh", *h), ("dh_last", "f32", e), ("dgate", *gate), ("dx", *x),
-                              ("dh0", "f32", e))}
+        n, D = self.B * self.T, self.D
+        gate = (self.dtype, n, self.gate_stride or D, D)
+        x = (self.dtype, n, self.x_stride or D, D)
+        h = (self.dtype, n, self.h_stride or D, D)
+        state = ("f32", self.B, D, D)
+        lens = ("len", "i32", 1, self.B, self.B)
+        states = ("states", "f32", self.B * -(-self.T // SPEC_SCAN_CHUNK), D, D)
+        return {"scan": (("gate", *gate), ("x", *x), ("h0", *state), lens, ("h", *h),
+                         ("h_last", *state), states),
+                "scan_grad": (("gate", *gate), ("x", *x), ("h0", *state), lens, states,
+                              ("dh", *h), ("dh_last", *state), ("dgate", *gate), ("dx", *x),
+                              ("dh0", *state))}
 
 
 @dataclass(frozen=True)
@@ -268,14 +264,15 @@ class W4Params(_Held):
                             self.x_rows, 0, self.x_stride, self.base_stride, self.out_stride)
 
     def _tensors(self):
-        rest = (("wq", "u8", self.V * (-(-self.r // 128) * 64)),
-                ("wscale", self.scale_dtype, self.V * (self.r // max(self.group, 1))),
-                ("base", self.base_dtype, _span(self.B, self.base_stride, self.V)),
-                ("out", self.out_dtype, _span(self.B, self.out_stride, self.V)))
-        prev = ("prev", "i32", self.B)
-        return {"rows": (("x", self.dtype, _span(self.B, self.x_stride, self.r)), prev, *rest),
-                "lookup": (("x", self.dtype, _span(self.x_rows, self.x_stride, self.r)), prev,
-                           *rest)}
+        codes, groups = -(-self.r // 128) * 64, self.r // max(self.group, 1)
+        rest = (("wq", "u8", self.V, codes, codes),
+                ("wscale", self.scale_dtype, self.V, groups, groups),
+                ("base", self.base_dtype, self.B, self.base_stride or self.V, self.V),
+                ("out", self.out_dtype, self.B, self.out_stride or self.V, self.V))
+        prev = ("prev", "i32", 1, self.B, self.B)
+        x = self.x_stride or self.r
+        return {"rows": (("x", self.dtype, self.B, x, self.r), prev, *rest),
+                "lookup": (("x", self.dtype, self.x_rows, x, self.r), prev, *rest)}
 
 
 @dataclass(frozen=True)
@@ -294,13 +291,13 @@ class ProbsParams(_Held):
                                self.target_stride, self.draft_stride)
 
     def _tensors(self):
-        bk = self.B * self.K
-        return {"verify": (("target", self.dtype, _span(bk + self.B, self.target_stride, self.V)),
-                           ("draft_probs", self.draft_dtype, _span(bk, self.draft_stride, self.V)),
-                           ("draft", "i32", bk), ("u_accept", "f32", bk),
-                           ("u_draw", "f32", self.B), ("verify_len", "i32", self.B),
-                           ("out", "i32", bk + self.B), ("tau", "i32", self.B),
-                           ("p_draft", "f32", bk), ("q_draft", "f32", bk))}
+        B, K, V = self.B, self.K, self.V
+        return {"verify": (("target", self.dtype, B * (K + 1), self.target_stride or V, V),
+                           ("draft_probs", self.draft_dtype, B * K, self.draft_stride or V, V),
+                           ("draft", "i32", B, K, K), ("u_accept", "f32", B, K, K),
+                           ("u_draw", "f32", 1, B, B), ("verify_len", "i32", 1, B, B),
+                           ("out", "i32", B, K + 1, K + 1), ("tau", "i32", 1, B, B),
+                           ("p_draft", "f32", B, K, K), ("q_draft", "f32", B, K, K))}
 
 
 def _ptr(t):
@@ -454,21 +451,55 @@ def _torch():
     global _TORCH
     if _TORCH is None:
         import torch
-        # the stream's handle without making a Stream object for it, where torch offers it
+        # the device and the stream's handle without further Python, where torch offers it
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda d: torch.cuda.current_stream(d).cuda_stream)
-        _TORCH = (torch.cuda.current_device, raw,
+        torch.cuda.init()
+        _TORCH = (getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device), raw,
                   {"f32": torch.float32, "bf16": torch.bfloat16, "i32": torch.int32,
                    "u8": torch.uint8})
     return _TORCH
 
 
-def _run(fn, p, args, tensors, ws, stream):
+def _check_rows(name, t, rows, stride, width):
+    """A tensor's rows must lie where the call looks for them: `stride` elements
+    apart, one after the other over all leading axes.  A flat tensor, or whole
+    storage with longer rows, will do if it holds them."""
+    need = 0 if rows <= 0 else (rows - 1) * stride + width
+    last = t.storage_offset() + need
+    if t.untyped_storage().nbytes() < last * t.element_size():
+        raise ValueError(f"{name} holds too few elements, expected {rows} rows of {width}")
+    if need == 0:
+        return
+    if t.dim() == 0 or t.stride(-1) != 1 and t.size(-1) != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    if t.dim() == 1:
+        if t.numel() < need:
+            raise ValueError(f"{name} holds {t.numel()} elements, expected {need}")
+        return
+    if t.size(-1) < width or t.numel() // t.size(-1) < rows:
+        raise ValueError(f"{name} is {tuple(t.shape)}, expected {rows} rows of {width}")
+    apart = stride  # what one step along the axis, from the last but one outwards, moves
+    for k in range(t.dim() - 2, -1, -1):
+        if t.size(k) != 1 and t.stride(k) != apart:
+            raise ValueError(f"{name}: its rows are not {stride} elements apart")
+        apart *= t.size(k)
+
+
+def _typed(p, call):
+    """The tensors of a call as _run looks at them: (torch dtype, row stride,
+    elements of all rows), and what _check_rows wants."""
+    types = (_TORCH or _torch())[2]
+    args = tuple((types[dt], stride, rows * stride, name, dt, rows, width)
+                 for name, dt, rows, stride, width in p._args[call])
+    p._ready[call] = args
+    return args
+
+
+def _run(fn, p, call, tensors, ws, stream):
     """One operator's call, after the checks that the C side cannot make.
-    Tensors, workspace and stream must belong to the current device.  The
-    elements of a tensor must be reachable from its data pointer by the strides
-    the parameters give, so a strided view passes if its storage holds them."""
-    current, raw, types = _TORCH or _torch()
+    Tensors, workspace and stream must belong to the current device."""
+    current, raw, _ = _TORCH or _torch()
     dev = current()
     if stream is None:
         st = raw(dev)
@@ -477,19 +508,18 @@ def _run(fn, p, args, tensors, ws, stream):
     else:
         raise ValueError("the stream belongs to another device than the current one")
     ptr = []
-    for t, (name, dt, least) in zip(tensors, args):
+    for t, (dtype, stride, total, name, dt, rows, width) in zip(tensors, p._ready.get(call)
+                                                                or _typed(p, call)):
         if t is None:
             ptr.append(None)
             continue
+        if t.dtype is not dtype:
+            raise ValueError(f"{name} is {t.dtype}, expected {dt}")
         if t.get_device() != dev:
             raise ValueError(f"{name} is on {t.device}, the call on cuda:{dev}")
-        if t.dtype is not types[dt]:
-            raise ValueError(f"{name} is {t.dtype}, expected {dt}")
-        if not t.is_contiguous() and t.stride(-1) != 1:
-            raise ValueError(f"{name}: the elements of a row must be contiguous")
-        if t.numel() < least and (t.untyped_storage().nbytes() // t.element_size()
-                                  - t.storage_offset()) < least:
-            raise ValueError(f"{name} holds {t.numel()} elements, expected {least}")
+        # dense rows, the common case, in three looks
+        if not (t.is_contiguous() and t.numel() >= total and t.size(-1) == stride):
+            _check_rows(name, t, rows, stride, width)
         ptr.append(t.data_ptr())
     if ws.get_device() != dev or ws.nbytes < p._need:
         raise SpecError(SPEC_ERR_WORKSPACE, f"{fn}: workspace too small or on another device")
@@ -500,32 +530,32 @@ def _run(fn, p, args, tensors, ws, stream):
 
 def embed(p: EmbedParams, table, ids, rows, ws, stream=None):
     """spec_embed: rows[i] = scale * table[ids[i]] (ids int32; -1 gives zeros)."""
-    _run("spec_embed", p, p._args["embed"], (table, ids, rows), ws, stream)
+    _run("spec_embed", p, "embed", (table, ids, rows), ws, stream)
 
 
 def embed_grad(p: EmbedParams, ids, drows, dtable, ws, stream=None):
     """spec_embed_grad: dtable[v] (+)= scale * sum of drows[i] with ids[i] = v."""
-    _run("spec_embed_grad", p, p._args["embed_grad"], (ids, drows, dtable), ws, stream)
+    _run("spec_embed_grad", p, "embed_grad", (ids, drows, dtable), ws, stream)
 
 
 def gated_scan(p: ScanParams, gate, x, h0, len, h, h_last, states, ws, stream=None):
     """spec_gated_scan: h_t = f_t h_{t-1} + (1 - f_t) x_t, f = sigmoid(gate).
     h0, len, h, h_last and states may be None."""
-    _run("spec_gated_scan", p, p._args["scan"], (gate, x, h0, len, h, h_last, states), ws, stream)
+    _run("spec_gated_scan", p, "scan", (gate, x, h0, len, h, h_last, states), ws, stream)
 
 
 def gated_scan_grad(p: ScanParams, gate, x, h0, len, states, dh, dh_last, dgate, dx, dh0, ws,
                     stream=None):
     """spec_gated_scan_grad: the gradients of gate, x and h0 from dh and dh_last.
     h0, len, dh_last and dh0 may be None; states as gated_scan wrote them."""
-    _run("spec_gated_scan_grad", p, p._args["scan_grad"],
+    _run("spec_gated_scan_grad", p, "scan_grad",
          (gate, x, h0, len, states, dh, dh_last, dgate, dx, dh0), ws, stream)
 
 
 def bias_w4(p: W4Params, x, prev, wq, wscale, base, out, ws, stream=None):
     """spec_bias_w4: out = base + X . W with W in 4 bits (X[b] = x[prev[b]] or
     x[b]).  prev and base may be None."""
-    _run("spec_bias_w4", p, p._args["rows" if prev is None else "lookup"],
+    _run("spec_bias_w4", p, "rows" if prev is None else "lookup",
          (x, prev, wq, wscale, base, out), ws, stream)
 
 
@@ -554,7 +584,7 @@ def verify_probs(p: ProbsParams, target, draft_probs, draft, u_accept, u_draw, v
                  tau, p_draft, q_draft, ws, stream=None):
     """spec_verify_probs: verification from probabilities and given uniforms.
     verify_len, p_draft and q_draft may be None."""
-    _run("spec_verify_probs", p, p._args["verify"],
+    _run("spec_verify_probs", p, "verify",
          (target, draft_probs, draft, u_accept, u_draw, verify_len, out, tau, p_draft, q_draft),
          ws, stream)
 

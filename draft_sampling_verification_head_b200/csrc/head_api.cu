@@ -65,6 +65,7 @@ spec_status check_w4(const spec_w4_params* p, spec_w4_params* d) {
       p->reserved != 0 || !good_stride(p->x_stride, p->r) || !good_stride(p->base_stride, p->V) ||
       !good_stride(p->out_stride, p->V))
     return SPEC_ERR_INVALID_ARG;
+  if (p->B > (1 << 16) || p->V > (1 << 30)) return SPEC_ERR_UNSUPPORTED;  // grid and index limits
   if ((p->group != 32 && p->group != 64 && p->group != 128) || p->r % p->group != 0) {
     fprintf(stderr, "specdec: 4-bit weights come in groups of 32, 64 or 128 features that divide "
                     "the rank\n");
@@ -82,6 +83,7 @@ spec_status check_probs(const spec_probs_params* p, spec_probs_params* d) {
       !is_dtype(p->draft_dtype) || p->reserved != 0 || !good_stride(p->target_stride, p->V) ||
       !good_stride(p->draft_stride, p->V))
     return SPEC_ERR_INVALID_ARG;
+  if (p->V > (1 << 30)) return SPEC_ERR_UNSUPPORTED;  // token indices of a tile fit 32 bits
   *d = *p;
   if (d->target_stride == 0) d->target_stride = d->V;
   if (d->draft_stride == 0) d->draft_stride = d->V;

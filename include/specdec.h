@@ -393,9 +393,9 @@ spec_status spec_gated_scan_grad(const spec_scan_params *p, const void *gate, co
                                  float *dh0, void *workspace, spec_stream_t stream);
 
 typedef struct {
-  int32_t B;            /* rows, >= 1 (fast up to 16) */
+  int32_t B;            /* rows, 1 .. 65536; taken 16 at a time */
   int32_t r;            /* features, a multiple of group, up to 65536 */
-  int32_t V;            /* vocabulary, >= 1 */
+  int32_t V;            /* vocabulary, 1 .. 2^30 */
   int32_t group;        /* features that share a scale: 32, 64 or 128 */
   int32_t dtype;        /* spec_dtype of x */
   int32_t scale_dtype;  /* spec_dtype of wscale */
@@ -443,7 +443,7 @@ spec_status spec_w4_quantize(const spec_w4_params *p, const void *W, int32_t w_d
 typedef struct {
   int32_t B;              /* batch rows, >= 1 */
   int32_t K;              /* block length, 1 .. 1024 */
-  int32_t V;              /* vocabulary, >= 1 */
+  int32_t V;              /* vocabulary, 1 .. 2^30 */
   int32_t dtype;          /* spec_dtype of target */
   int32_t draft_dtype;    /* spec_dtype of draft_probs */
   int32_t reserved;       /* 0 */

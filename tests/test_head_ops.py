@@ -238,7 +238,8 @@ def test_w4_host_checks():
                dict(prev=FAKE, x_rows=0), dict(wq=ctypes.c_void_p(0x10008)),
                dict(out=ctypes.c_void_p(0x10002))):
         assert run(**kw) == bad, kw
-    for kw in (dict(group=16), dict(group=48, r=96), dict(r=80), dict(group=128)):
+    for kw in (dict(group=16), dict(group=48, r=96), dict(r=80), dict(group=128), dict(B=65537),
+               dict(V=2**30 + 1)):
         assert run(**kw) == uns, kw
     assert run(w=None) == sd.SPEC_ERR_WORKSPACE
     p = sd.W4Params(B=1, r=64, V=10, group=32)
@@ -259,7 +260,51 @@ def test_verify_probs_host_checks():
 
     for kw in (dict(B=0), dict(K=0), dict(K=1025), dict(V=0), dict(target_stride=9), dict(draft_stride=-1)):
         assert run(**kw) == bad, kw
+    assert run(V=2**30 + 1) == sd.SPEC_ERR_UNSUPPORTED
     for k in (0, 1, 2, 3, 4, 6, 7):
         assert run(at=k) == bad, k
     assert run(at=2, v=ctypes.c_void_p(0x10002)) == bad
     assert run(w=None) == sd.SPEC_ERR_WORKSPACE
+
+
+# ---- the binding's checks of layouts (no GPU: they look at shapes and strides only) ----
+def _rows_ok(t, rows, stride, width):
+    try:
+        sd._check_rows("t", t, rows, stride, width)
+        return True
+    except ValueError:
+        return False
+
+
+def test_binding_accepts_rows_where_the_call_looks_for_them():
+    import torch
+    ok = _rows_ok
+    assert ok(torch.zeros(6, 5), 6, 5, 5) and ok(torch.zeros(30), 6, 5, 5)
+    assert ok(torch.zeros(2, 3, 5), 6, 5, 5)
+    assert ok(torch.zeros(6, 8), 6, 8, 5)            # whole storage, longer rows
+    assert ok(torch.zeros(6, 8)[:, :5], 6, 8, 5)     # its view
+    assert ok(torch.zeros(2, 3, 8)[..., :5], 6, 8, 5)
+    assert ok(torch.zeros(1, 5).expand(1, 5), 1, 5, 5) and ok(torch.empty(0), 0, 5, 5)
+    assert ok(torch.zeros(6, 1), 6, 1, 1)
+
+
+def test_binding_refuses_rows_that_lie_elsewhere():
+    import torch
+    ok = _rows_ok
+    assert not ok(torch.zeros(6, 8)[:, :5], 6, 5, 5)          # dense rows are expected
+    assert not ok(torch.zeros(6, 5), 6, 8, 5)                 # wider ones are
+    assert not ok(torch.zeros(5, 6).t(), 6, 5, 5)             # columns
+    assert not ok(torch.zeros(2, 4, 5)[:, :3], 6, 5, 5)       # a gap between sequences
+    assert not ok(torch.zeros(5, 5), 6, 5, 5) and not ok(torch.zeros(29), 6, 5, 5)
+    assert not ok(torch.zeros(1, 5).expand(6, 5), 6, 5, 5)    # one row for all
+    assert not ok(torch.zeros(12)[::2], 1, 6, 6)
+    assert not ok(torch.zeros(4, 8)[:, :4], 4, 4, 4)          # drafts of a longer block
+
+
+def test_parameter_objects_copy_with_a_structure_of_their_own():
+    import copy
+    import pickle
+    p = sd.ProbsParams(B=2, K=3, V=10)
+    assert p.c().V == 10
+    for q in (copy.copy(p), copy.deepcopy(p), pickle.loads(pickle.dumps(p))):
+        assert q == p and q.c() is not p.c() and q.c().V == 10
