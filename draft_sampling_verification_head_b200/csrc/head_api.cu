@@ -40,6 +40,7 @@ spec_status check_embed(const spec_embed_params* p, spec_embed_params* d) {
       !std::isfinite(p->scale) || p->reserved != 0 || !good_stride(p->table_stride, p->D) ||
       !good_stride(p->row_stride, p->D))
     return SPEC_ERR_INVALID_ARG;
+  if (p->n > (1 << 30)) return SPEC_ERR_UNSUPPORTED;  // ends of pieces fit 32 bits
   *d = *p;
   if (d->table_stride == 0) d->table_stride = d->D;
   if (d->row_stride == 0) d->row_stride = d->D;

@@ -312,7 +312,7 @@ spec_status spec_l2_persist(const void *ptr, size_t bytes, spec_stream_t stream)
 #define SPEC_WORKSPACE_MIN 256
 
 typedef struct {
-  int32_t n;             /* tokens, >= 0 */
+  int32_t n;             /* tokens, 0 .. 2^30 */
   int32_t V;             /* rows of the table, >= 1 */
   int32_t D;             /* row width, 1 .. 65536 */
   int32_t dtype;         /* spec_dtype of the table (lookup) or of its gradient */

@@ -729,6 +729,156 @@ def test_operators_share_a_workspace_with_the_cycle():
     assert torch.equal(first, cycle())
 
 
+@pytest.mark.parametrize("acc", [False, True])
+@pytest.mark.parametrize("bad", [-2, 50, 2**31 - 1, -2**31])
+def test_embed_grad_of_many_positions_reports_tokens_out_of_range(bad, acc):
+    """The others' sums are as without it."""
+    n, V, D = 9000, 50, 12
+    ids = torch.randint(0, V, (n,), generator=gen(5), dtype=torch.int32)
+    ids[[0, 4111, n - 1]] = bad
+    st, _ = _embed_grad(n, V, D, "f32", "bf16", 0, acc, ids, gen(6))
+    assert st == sd.SPEC_ERR_TOKEN_RANGE
+
+
+# ---------------------------------------------------------------------------
+# rows whose offsets pass 32 bits
+# ---------------------------------------------------------------------------
+FAR = 2**30  # elements between rows: the fifth one lies past 2^32
+
+
+@pytest.fixture(scope="module")
+def far_buffers():
+    if torch.cuda.get_device_properties(0).total_memory < 40 * 2**30:
+        pytest.skip("needs 18 GB")
+    yield [torch.empty(4 * FAR + 2**23, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    torch.cuda.empty_cache()
+
+
+def far(buf, t, stride, at=0):
+    """The rows of t (or space for them) `stride` elements apart: the flat view that a
+    call takes, and its rows."""
+    n, d = t.shape
+    flat = buf[at:at + (n - 1) * stride + d]
+    rows = flat.as_strided((n, d), (stride, 1))
+    rows.copy_(t)
+    return flat, rows
+
+
+def test_embed_far_rows(far_buffers):
+    a, b = far_buffers
+    V, D, n = 5, 72, 5
+    t, ids = rand(gen(1), V, D, dtype="bf16"), torch.tensor([4, 0, 3, 4, 1], dtype=torch.int32).cuda()
+    dense = sd.EmbedParams(n=n, V=V, D=D, scale=0.5)
+    p = sd.EmbedParams(n=n, V=V, D=D, scale=0.5, table_stride=FAR, row_stride=FAR)
+    ws, want = sd.make_workspace(p), torch.empty(n, D, dtype=torch.bfloat16, device="cuda")
+    sd.embed(dense, t, ids, want, ws)
+    table, _ = far(a, t, FAR)
+    out, rows = far(b, torch.zeros_like(want), FAR)
+    sd.embed(p, table, ids, out, ws)
+    assert torch.equal(rows, want)
+    sd.embed_grad(dense, ids, want, t, ws)
+    dtable, drows = far(a, torch.ones_like(t), FAR)
+    sd.embed_grad(p, ids, out, dtable, ws)
+    assert torch.equal(drows, t) and sd.sync_status(ws) == sd.SPEC_OK
+
+
+def test_embed_grad_far_rows_sorted(far_buffers):
+    a, b = far_buffers
+    n, V, D, stride = 2050, 5, 40, 2**21
+    assert (n - 1) * stride > 2**32 - 1 and n > 2048
+    drows, t = rand(gen(1), n, D, dtype="bf16"), torch.empty(V, D, dtype=torch.bfloat16, device="cuda")
+    ids = torch.randint(0, V, (n,), generator=gen(2), dtype=torch.int32).cuda()
+    p = sd.EmbedParams(n=n, V=V, D=D, table_stride=FAR, row_stride=stride)
+    ws = sd.make_workspace(p)
+    sd.embed_grad(sd.EmbedParams(n=n, V=V, D=D), ids, drows, t, ws)
+    flat, _ = far(a, drows, stride)
+    dtable, got = far(b, torch.ones_like(t), FAR)
+    sd.embed_grad(p, ids, flat, dtable, ws)
+    assert torch.equal(got, t) and sd.sync_status(ws) == sd.SPEC_OK
+
+
+def test_gated_scan_far_rows(far_buffers):
+    a, b = far_buffers
+    T, D = 5, 70
+    g = gen(3)
+    gate, x, dh = (rand(g, T, D, dtype="bf16") for _ in range(3))
+    h0 = rand(g, 1, D)
+    p = sd.ScanParams(B=1, T=T, D=D, gate_stride=FAR, x_stride=FAR, h_stride=FAR)
+    dense = sd.ScanParams(B=1, T=T, D=D)
+    ws = sd.make_workspace(p)
+    h, dg, dx = (torch.empty_like(gate) for _ in range(3))
+    last, states, d0 = (torch.empty(1, D, device="cuda") for _ in range(3))
+    sd.gated_scan(dense, gate, x, h0, None, h, last, states, ws)
+    sd.gated_scan_grad(dense, gate, x, h0, None, states, dh, last, dg, dx, d0, ws)
+    fg, fx, fd = far(a, gate, FAR)[0], far(a, x, FAR, 256)[0], far(a, dh, FAR, 512)[0]
+    fh, got = far(b, torch.zeros_like(h), FAR)
+    last2, states2, d02 = (torch.empty(1, D, device="cuda") for _ in range(3))
+    sd.gated_scan(p, fg, fx, h0, None, fh, last2, states2, ws)
+    assert torch.equal(got, h) and torch.equal(last, last2) and torch.equal(states, states2)
+    (f1, got1), (f2, got2) = far(b, torch.ones_like(h), FAR), far(b, torch.ones_like(h), FAR, 256)
+    sd.gated_scan_grad(p, fg, fx, h0, None, states, fd, last, f1, f2, d02, ws)
+    assert torch.equal(got1, dg) and torch.equal(got2, dx) and torch.equal(d0, d02)
+    assert sd.sync_status(ws) == sd.SPEC_OK
+
+
+def test_bias_w4_far_rows(far_buffers):
+    a, b = far_buffers
+    B, r, V = 5, 64, 75
+    g = gen(4)
+    codes, wq, wscale = w4_inputs(B, r, V, 64, "bf16", "f32", g)
+    x, base = rand(g, B, r, dtype="bf16"), rand(g, B, V, dtype="bf16")
+    kw = dict(B=B, r=r, V=V, group=64, dtype="bf16", scale_dtype="f32", base_dtype="bf16", out_dtype="bf16")
+    dense, p = sd.W4Params(**kw), sd.W4Params(x_stride=FAR, base_stride=FAR, out_stride=FAR, **kw)
+    ws, want = sd.make_workspace(p), torch.empty_like(base)
+    sd.bias_w4(dense, x, None, wq, wscale, base, want, ws)
+    out, got = far(b, torch.zeros_like(base), FAR)
+    sd.bias_w4(p, far(a, x, FAR)[0], None, wq, wscale, far(a, base, FAR, 256)[0], out, ws)
+    assert torch.equal(got, want) and sd.sync_status(ws) == sd.SPEC_OK
+
+
+def test_bias_w4_codes_past_32_bits(far_buffers):
+    """The last tokens of a factor of more than 2^32 bytes, alone and among all."""
+    r, tail = 4096, 64
+    V = 2**32 // (r // 2) + 2 * tail
+    g = gen(5)
+    codes, wq, sc = w4_inputs(1, r, tail, 128, "bf16", "bf16", g)
+    allq = far_buffers[0].view(torch.uint8)[:V * (r // 2)].view(V, r // 2)
+    allq[:-tail].zero_()
+    allq[-tail:] = wq
+    scales = torch.zeros(V, r // 128, dtype=torch.bfloat16, device="cuda")
+    scales[-tail:] = sc
+    x = rand(g, 1, r, dtype="bf16")
+    kw = dict(B=1, r=r, group=128, dtype="bf16", scale_dtype="bf16", out_dtype="f32")
+    small, big = sd.W4Params(V=tail, **kw), sd.W4Params(V=V, **kw)
+    ws = sd.make_workspace(big)
+    want, got = torch.empty(1, tail, device="cuda"), torch.empty(1, V, device="cuda")
+    sd.bias_w4(small, x, None, wq, sc, None, want, ws)
+    sd.bias_w4(big, x, None, allq, scales, None, got, ws)
+    # the features may be split over another number of warps: fp32 sums of r terms
+    w = (codes.astype(np.float64) - 8) * np.repeat(np64(sc), 128, axis=1)
+    tol = 2 * r * U * (np.abs(w) @ np.abs(np64(x)[0]))
+    within(got[0, -tail:], np64(want)[0], tol)
+    assert bool((got[0, :-tail] == 0).all()) and sd.sync_status(ws) == sd.SPEC_OK
+
+
+def test_verify_probs_far_rows(far_buffers):
+    a, b = far_buffers
+    B, K, V = 1, 4, 1003
+    for seed in range(6):
+        t, q, d, ua, ud, _ = probs_inputs(B, K, V, "bf16", "bf16", seed, sigma=0.2)
+        if seed < 3:
+            ua[:] = 0.0  # all accepted: the bonus row is the far one
+        want = run_probs(t, q, d, ua, ud, None, (0, 0), "bf16", "bf16")
+        p = sd.ProbsParams(B=B, K=K, V=V, dtype="bf16", draft_dtype="bf16", target_stride=FAR, draft_stride=FAR)
+        ws = sd.make_workspace(p)
+        out, tau = torch.empty(B, K + 1, dtype=torch.int32).cuda(), torch.empty(B, dtype=torch.int32).cuda()
+        pd, qd = torch.empty(B, K).cuda(), torch.empty(B, K).cuda()
+        sd.verify_probs(p, far(a, t[0].cuda(), FAR)[0], far(b, q[0].cuda(), FAR)[0], d.cuda(), ua.cuda(),
+                        ud.cuda(), None, out, tau, pd, qd, ws)
+        for got, w in zip((sd.sync_status(ws), out.cpu().numpy(), tau.cpu().numpy(), np64(pd), np64(qd)), want):
+            assert np.array_equal(got, w, equal_nan=isinstance(w, np.ndarray) and w.dtype == np.float64)
+
+
 def test_binding_refuses_what_the_library_cannot_see():
     p = sd.EmbedParams(n=4, V=10, D=8, dtype="f32", row_dtype="f32")
     ws = sd.make_workspace(p)

@@ -192,6 +192,14 @@ def test_embed_without_tokens_is_no_work():
     assert sd.last_launch_count() == 0
 
 
+@pytest.mark.parametrize("fn", ["spec_embed", "spec_embed_grad"])
+def test_embed_refuses_more_tokens_than_its_indices_hold(fn):
+    p = _embed(n=2**30 + 1)
+    assert _call(fn, p, FAKE, FAKE, FAKE, FAKE, None) == sd.SPEC_ERR_UNSUPPORTED
+    assert sd.workspace_size(p) == 0
+    assert sd.workspace_size(_embed(n=2**30)) > 0
+
+
 def _scan(**kw):
     d = dict(B=2, T=5, D=8)
     d.update(kw)
