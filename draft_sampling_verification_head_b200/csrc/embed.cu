@@ -188,11 +188,12 @@ SPEC_DEV void zero_rows(const spec_embed_params& p, TT* dtable, int64_t v0, int6
   }
 }
 
-constexpr int kDirect = 2048;     // most positions that are not sorted
+constexpr int kDirect = 4096;     // most positions that are not sorted
 constexpr int kZeroRows = 1024;   // most table rows a CTA zeroes beside them
 
 constexpr int kDirectWarps = 16;
-constexpr int kRun = kDirect / kDirectWarps;  // positions a warp looks through
+constexpr int kRun = kDirect / kDirectWarps;  // most positions a warp looks through
+constexpr int kIds = 4;                       // of them per lane at a time
 
 // CTAs 0 .. n - 1: the first position of a token sums the rows of all positions
 // that name it; its warps list those of a run of positions each.  The CTAs after
@@ -217,26 +218,29 @@ __global__ void __launch_bounds__(32 * kDirectWarps, 2)
     return;
   }
   __shared__ float part[kDirectWarps][32 * kCols];
-  __shared__ int32_t list[kDirectWarps][kRun];
+  __shared__ uint16_t list[kDirectWarps][kRun];
   const int i = blockIdx.x, id = __ldg(ids + i);
   if (id < 0 || id >= p.V) {
     if (id != -1 && tid == 0) report_error(hdr, SPEC_ERR_TOKEN_RANGE, SITE_TOKEN_RANGE, i, id);
     return;
   }
   // the warp's run of positions: those that name the token, in order
+  const int run = (n + 32 * kDirectWarps - 1) / (32 * kDirectWarps) * 32;
   int count = 0;
   bool before = false;
+  for (int k0 = 0; k0 < run; k0 += 32 * kIds) {
 #pragma unroll
-  for (int k = 0; k < kRun / 32; ++k) {
-    const int j = warp * kRun + k * 32 + lane;
-    const bool same = j < n && __ldg(ids + j) == id;
-    before |= same && j < i;
-    const uint32_t m = __ballot_sync(0xffffffffu, same);
-    if (same) list[warp][count + __popc(m & ((1u << lane) - 1))] = j;
-    count += __popc(m);
+    for (int k = 0; k < kIds; ++k) {
+      const int in = k0 + k * 32 + lane, j = warp * run + in;
+      const bool same = in < run && j < n && __ldg(ids + j) == id;
+      before |= same && j < i;
+      const uint32_t m = __ballot_sync(0xffffffffu, same);
+      if (same) list[warp][count + __popc(m & ((1u << lane) - 1))] = (uint16_t)j;
+      count += __popc(m);
+    }
   }
   if (__syncthreads_or(before)) return;
-  const bool alone = !__syncthreads_or(count > (warp == i / kRun));
+  const bool alone = !__syncthreads_or(count > (warp == i / run));
   if (alone) {  // the common case: one row
     for (int block = warp; block * kCols * 32 < p.D; block += kDirectWarps) {
       const Columns<kWide> c(block, lane, 32, p.D);
@@ -285,6 +289,7 @@ constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kDigits = 512;                       // 9 bits a pass
 constexpr int kTile = 2048;                        // positions ranked together
 constexpr int kRounds = kTile / kSortThreads;      // of 32 neighbouring positions per warp
+static_assert(kDirect <= 65536, "positions of the list fit 16 bits");
 static_assert(kDigits == kSortThreads, "one thread per digit");
 
 struct SortArgs {

@@ -25,7 +25,7 @@ namespace {
 constexpr int kChunk = SPEC_SCAN_CHUNK;  // steps per piece
 constexpr int kMaxCluster = 8;           // CTAs per cluster (portable limit)
 constexpr int kSoloWarps = 8;            // warps per CTA where each has a job of its own
-constexpr int kSplitSteps = 1024;        // shortest sequence whose steps are split
+constexpr int kSplitSteps = 5120;        // shortest sequence whose steps are split
 constexpr int kMinSegment = 64;          // shortest segment
 
 SPEC_DEV int len_of(const int32_t* len, int b, int T, WsHeader* hdr, bool say) {
@@ -748,7 +748,9 @@ int64_t jobs_of(const spec_scan_params& p, int V) {
 
 // Steps per segment where the steps are split, 0 where they are not.  Split
 // when clusters of every job would still leave SMs without a CTA and the steps
-// fill several of their windows; segments then give every SM about 16 warps.
+// fill five of their windows (one sequence of 256 bf16 channels, forward and
+// gradient: split 17 and 23 us at 4096 steps, 19 and 24 at 8192; in clusters 15
+// and 21, 25 and 36); segments then give every SM about 16 warps.
 int segment_steps(const spec_scan_params& p, int64_t jobs, int num_sms) {
   if (jobs * kMaxCluster >= num_sms || p.T < kSplitSteps) return 0;
   const int64_t segs = (16 * (int64_t)num_sms + jobs - 1) / jobs;

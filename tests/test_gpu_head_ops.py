@@ -68,7 +68,7 @@ def strided(t, extra):
 # lookup and its gradient
 # ---------------------------------------------------------------------------
 EMBED = [(1, 1, 1), (3, 7, 5), (64, 500, 256), (257, 33, 250), (5, 2, 1030), (1000, 3, 64),
-         (4097, 900, 36), (70, 100, 4104)]
+         (4097, 900, 36), (70, 100, 4104), (4096, 1500, 70), (2100, 3000, 256)]
 
 
 @pytest.mark.parametrize("pad", [0, 3, 8])
@@ -185,7 +185,9 @@ def test_embed_reports_tokens_out_of_range(bad):
 # gated recurrence
 # ---------------------------------------------------------------------------
 SCAN = [(1, 1, 1), (2, 1, 64), (64, 1, 256), (3, 5, 7), (1, 16, 33), (2, 17, 64), (2, 100, 130),
-        (5, 65, 2), (1, 1000, 66), (3, 2050, 31), (1, 5000, 8), (40, 33, 257)]
+        (5, 65, 2), (1, 1000, 66), (3, 2050, 31), (1, 5000, 8), (40, 33, 257),
+        # steps split over the GPU
+        (1, 6001, 8), (3, 5205, 31), (2, 5120, 66)]
 
 
 def scan_inputs(B, T, D, dtype, seed, ragged, pad=0, std=2.0):
@@ -308,7 +310,8 @@ def test_scan_steps_in_place_equal_the_sequence():
     within(state, np64(last), 2 * e)
 
 
-@pytest.mark.parametrize("B,T,D,dtype", [(1, 4099, 40, "bf16"), (2, 2048, 7, "f32"), (2, 700, 64, "bf16")])
+@pytest.mark.parametrize("B,T,D,dtype", [(1, 4099, 40, "bf16"), (2, 2048, 7, "f32"), (2, 700, 64, "bf16"),
+                                       (1, 6099, 40, "bf16"), (2, 5130, 7, "f32")])
 def test_scan_state_in_place_over_long_sequences(B, T, D, dtype):
     """The last state written over the first one: the same bits as apart."""
     gate, x, h0, _, _ = scan_inputs(B, T, D, dtype, 12, False)
