@@ -10,6 +10,14 @@
 // from, and the pieces are run once more from there.  Inputs are read once and
 // outputs written once, whatever the length; equal inputs give equal bits since
 // the joins are taken in a fixed order.
+//
+// What bounds it: bytes where jobs fill the GPU (forward, 256 x 256 x 1024 bf16:
+// 78 us, 5.2 TB/s), instruction issue and the joins' barriers in the gradient
+// (8 x 8192 x 1024 bf16: 175 us, 3.9 TB/s; about 45 instructions a pair of
+// elements, the issue slots half used), the chain of dependent steps and launches
+// where work is small.  Clusters of 16, of which only part fits the GPU, took
+// 96 us where 8 took 85; a cluster barrier in place of the counted stores 186
+// against 172.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -27,6 +35,7 @@ constexpr int kMaxCluster = 8;           // CTAs per cluster (portable limit)
 constexpr int kSoloWarps = 8;            // warps per CTA where each has a job of its own
 constexpr int kSplitSteps = 5120;        // shortest sequence whose steps are split
 constexpr int kMinSegment = 64;          // shortest segment
+constexpr int kStages = 2;               // pieces of a warp on their way, forward
 
 SPEC_DEV int len_of(const int32_t* len, int b, int T, WsHeader* hdr, bool say) {
   if (!len) return T;
@@ -419,12 +428,13 @@ SPEC_DEV Vec<V> segment_start(const ScanArgs& a, Joiner<V, 1>& sm, const Place& 
 
 // Forward.  W > 1: a cluster per job (a sequence's tile of 32 V channels) walks
 // the steps in windows of cluster * W pieces.  W = 1: a warp per job, a window is
-// one piece and nothing is joined.  The next window's inputs are requested
-// before the current one is joined.
+// one piece and nothing is joined.  Two windows' inputs are on their way while
+// one is computed (one instead of two: 256 x 256 x 1024 bf16 90 us, two 78, three
+// 78).
 template <typename T, int V, int W>
 struct ScanShared {
   Joiner<V, W> joiner;
-  Piece<T, V> gate[W == 1 ? kSoloWarps : W], x[W == 1 ? kSoloWarps : W];
+  Piece<T, V> gate[W == 1 ? kSoloWarps : W][kStages], x[W == 1 ? kSoloWarps : W][kStages];
 };
 
 template <typename T, int V, int W>
@@ -451,14 +461,15 @@ __global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), 2)
 
   const int window = C * W * kChunk;
   int t0 = at.t0 + (rank * W + warp) * kChunk;
-  auto request = [&](int t) {
+  auto request = [&](int t, int stage) {
     if (t < min(n, at.t1)) {
-      fetch(sm.gate[wid], gp + (int64_t)t * a.p.gate_stride, a.p.gate_stride, n - t, D - ct, a.wide);
-      fetch(sm.x[wid], xp + (int64_t)t * a.p.x_stride, a.p.x_stride, n - t, D - ct, a.wide);
+      fetch(sm.gate[wid][stage], gp + (int64_t)t * a.p.gate_stride, a.p.gate_stride, n - t, D - ct, a.wide);
+      fetch(sm.x[wid][stage], xp + (int64_t)t * a.p.x_stride, a.p.x_stride, n - t, D - ct, a.wide);
     }
     cp_async_commit();
   };
-  request(t0);
+#pragma unroll
+  for (int q = 0; q < kStages; ++q) request(t0 + q * window, q);
   join_init<V, W>(sm.joiner, C);
   if constexpr (W == 1) {
     if (a.nseg > 1) {
@@ -467,15 +478,15 @@ __global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), 2)
     }
   }
   const int nwin = (at.t1 - at.t0 + window - 1) / window;
-  for (int win = 0; win < nwin; ++win, t0 += window) {
+  for (int win = 0, stage = 0; win < nwin; ++win, t0 += window) {
     Vec<V> f[kChunk], z[kChunk], ma = Vec<V>::all(1.f), mc = Vec<V>::all(0.f);
-    cp_async_wait<0>();
+    cp_async_wait<kStages - 1>();
     __syncwarp();
     const int left = n - t0;  // steps of the piece that belong to the sequence
 #pragma unroll
     for (int k = 0; k < kChunk; ++k) {
-      gate_of<T, V>(sm.gate[wid].at[k][lane], f[k], z[k]);
-      z[k] = z[k] * raw_value<T, V>(sm.x[wid].at[k][lane]);
+      gate_of<T, V>(sm.gate[wid][stage].at[k][lane], f[k], z[k]);
+      z[k] = z[k] * raw_value<T, V>(sm.x[wid][stage].at[k][lane]);
     }
     if (left < kChunk) {  // the others leave the state as it is
 #pragma unroll
@@ -491,7 +502,8 @@ __global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), 2)
       mc = fma(f[k], mc, z[k]);
     }
     __syncwarp();
-    request(t0 + window);
+    request(t0 + kStages * window, stage);
+    stage ^= 1;
     Vec<V> s;
     join<V, W>(sm.joiner, win, warp, rank, C, ma, mc, carry, s, a.hdr);
     if (on && a.states && t0 < Tn)
@@ -810,8 +822,14 @@ cudaError_t by_shape(ScanArgs& a, bool grad, int num_sms, uint8_t* body, cudaStr
   a.nseg = 1;
   a.seg = a.p.T;
   *launches = 1;
-  // a warp per job where the sequence is one piece, or where jobs fill the GPU
-  if (a.p.T <= kChunk || jobs_of(a.p, V) >= 16 * (int64_t)num_sms)
+  // A warp per job where the sequence is one piece, or where jobs fill the GPU:
+  // forward from six an SM (bf16, 64 x 512 x 2048: 76 us, joined 86; at 4.3 an SM
+  // 82 against 61).  The gradient, whose warps hold too much for two pieces on
+  // their way, only where a CTA's window would stay half empty (1024 x 64 x 512:
+  // 90 us, joined 123; 512 x 128 x 1024: 169 against 158).
+  const int64_t jobs = jobs_of(a.p, V);
+  if (a.p.T <= kChunk || (grad ? a.p.T <= W * kChunk / 2 && jobs >= 16 * (int64_t)num_sms
+                               : jobs >= 6 * (int64_t)num_sms))
     return launch<T, V, 1>(a, grad, num_sms, st);
   a.seg = segment_steps(a.p, jobs_of(a.p, V), num_sms);
   if (a.seg == 0) {

@@ -187,7 +187,9 @@ def test_embed_reports_tokens_out_of_range(bad):
 SCAN = [(1, 1, 1), (2, 1, 64), (64, 1, 256), (3, 5, 7), (1, 16, 33), (2, 17, 64), (2, 100, 130),
         (5, 65, 2), (1, 1000, 66), (3, 2050, 31), (1, 5000, 8), (40, 33, 257),
         # steps split over the GPU
-        (1, 6001, 8), (3, 5205, 31), (2, 5120, 66)]
+        (1, 6001, 8), (3, 5205, 31), (2, 5120, 66),
+        # sequences that fill the GPU, short ones and longer ones
+        (1200, 40, 66), (300, 70, 200)]
 
 
 def scan_inputs(B, T, D, dtype, seed, ragged, pad=0, std=2.0):
