@@ -118,12 +118,22 @@ __host__ __device__ __forceinline__ int packed_byte(int k) {
 // into three bf16 parts, which together hold all its 24 bits, as columns of
 // their own, so its products are exact as well.
 //
-// Bytes bound it: the codes pass through once, two blocks of 128 features ahead
-// of the products in registers.  X is laid out beforehand (k_w4_x) as the
+// The codes pass through once, two blocks of 128 features ahead of the products
+// in registers; that is their floor in bytes.  X is laid out beforehand (k_w4_x) as the
 // fragments the warps read, and stays in the SMs' first-level caches, so the
 // warps of a CTA need not wait for one another.  Where the vocabulary gives few
 // CTAs, or much work to each, the warps split the features and join their sums
 // in order.
+//
+// What bounds it: one row is bound by the codes' latency and the launches (r 256,
+// V 129280: 12.3 us); 16 rows by unpacking and multiplying, which the loads
+// overlap only in part (r 4096, V 151936: 123 us, 2.7 TB/s, 160 TFLOP/s.  Without
+// the products 90 us, without the weights' loads 84, without any loads 76, without
+// the sums' way out 108).  Registers allow 16 warps an SM.  Slower were: a tile of
+// tokens per warp or three CTAs an SM (150 to 175), a block's X or the codes staged
+// in shared memory (210, 126), persistent CTAs (140), and the fifth-generation
+// tensor cores with the codes unpacked into tensor memory, where the unpacking
+// threads' chain of waits costs more than the products save (166).
 // ----------------------------------------------------------------------------
 constexpr int kWarps = kThreads / 32;
 
@@ -324,7 +334,8 @@ __global__ void __launch_bounds__(kThreads, NT <= 3 ? 2 : 1)
 }
 static_assert(kTokens == 32, "the epilogue gives every lane a token");
 
-// One thread per token and 128 features, reading W's columns.
+// One thread per token and 128 features, reading W's columns: neighbouring threads
+// read neighbouring tokens.  Run once per factor, so its time is not on any path.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
     k_w4_quantize(spec_w4_params p, const T* __restrict__ W, uint8_t* wq, void* wscale) {
@@ -367,7 +378,7 @@ __global__ void __launch_bounds__(kThreads)
 
 }  // namespace
 
-constexpr int kSteps = 16;  // blocks of 128 features a warp goes through, about
+constexpr int kSteps = 16;  // blocks of 128 features a warp goes through, at most
 
 // Tiles of eight columns for up to 16 rows of X.
 static int column_tiles(const spec_w4_params& p) {
@@ -387,8 +398,10 @@ static cudaError_t product(const spec_w4_params& p, const uint4* xf, const uint8
                            const void* wscale, const void* base, void* out, int rows, int parts,
                            int num_sms, cudaStream_t st) {
   const int nkb = (p.r + 127) / 128;
-  // warps split the features while the tokens give fewer than two CTAs per SM,
-  // and until a CTA's work is short, so that the last ones to run end together
+  // warps split the features while the tokens give fewer than two CTAs per SM
+  // (4 rows, r 4096, V 8000: 15 us, unsplit 25), and until a CTA's work is short,
+  // so that the last ones to run end together (16 rows, r 4096, V 151936, groups of
+  // 64: 152 us, unsplit 169)
   int split = 1;
   while (split < kWarps && 2 * split <= nkb &&
          (nkb / split > kSteps ||

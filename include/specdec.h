@@ -336,8 +336,8 @@ spec_status spec_embed(const spec_embed_params *p, const void *table, const int3
                        void *rows, void *workspace, spec_stream_t stream);
 
 /* Its gradient: dtable[v] (+)= scale * sum of drows[i] over the i with
- * ids[i] = v.  The tokens are sorted first, so each table row is written once,
- * by fp32 sums in a fixed order (ascending i, in pieces joined in order), rounded once.  With
+ * ids[i] = v.  Each table row is written once, by fp32 sums in a fixed order
+ * (ascending i, in pieces joined in order), rounded once.  With
  * accumulate = 0 every table row is written (rows no token names become 0);
  * with 1 only the rows named by a token are touched.  Ids outside [0, V) add
  * nothing; all but -1 are reported as SPEC_ERR_TOKEN_RANGE. */
