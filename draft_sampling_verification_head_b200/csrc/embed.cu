@@ -606,39 +606,36 @@ __global__ void __launch_bounds__(kThreads)
     put_row<kWide>(a.p, dtable, cur, c, acc);
 }
 
-// One CTA per piece in which a run begins that goes on after it: the sums of
-// its parts, the warps taking a stretch of them each.  The longest run's latency
-// bounds it (12 us behind the sums at 131072 positions with Zipf tokens).
+// A warp per piece and block of columns: if a run begins in the piece that goes on
+// after it, the sum of the run's parts.  A run through many pieces is summed by
+// the CTA together, a stretch of the parts per warp; no two of them begin among
+// the pieces of one CTA.  Latency bounds it: the keys at the borders, the keys of
+// the pieces after, the parts.
+constexpr int kJoinWarps = kThreads / 32;
+constexpr int kManyParts = 16;
+static_assert(kManyParts >= kJoinWarps && kManyParts <= 32, "one long run per CTA, seen by one look");
+
 template <bool kWide, typename TT>
 __global__ void __launch_bounds__(kThreads) k_grad_join(SumArgs a, TT* dtable) {
-  __shared__ float sums[kThreads / 32][32 * kCols];
-  const int m = blockIdx.x, n = a.p.n, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t j0 = (int64_t)m * a.piece, j1 = j0 + a.piece;
+  __shared__ float sums[kJoinWarps][32 * kCols];
+  __shared__ int long_piece;
+  const int n = a.p.n, V = a.p.V, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int m = blockIdx.x * kJoinWarps + warp;
+  const Columns<kWide> c(blockIdx.y, lane, 32, a.p.D);
+  if (threadIdx.x == 0) long_piece = -1;
+  __syncthreads();
   grid_dependency_wait();
-  if (j1 >= n) return;
-  const int key = __ldg(a.keys + j1);
-  if (key >= a.p.V || __ldg(a.keys + j1 - 1) != key ||
-      (j0 > 0 && __ldg(a.keys + j0 - 1) == key))
-    return;
-  int more = 0;  // pieces after this one into which the run goes
-  for (int q0 = m + 1;; q0 += kThreads) {
-    const int64_t q = (int64_t)q0 + threadIdx.x;
-    const int got = __syncthreads_count(q < a.pieces && __ldg(a.keys + q * a.piece) == key);
-    more += got;
-    if (got < kThreads) break;
-  }
-  const int per = (more + 1 + kThreads / 32 - 1) / (kThreads / 32);
-  const int q0 = min(warp * per, more + 1), q1 = min(q0 + per, more + 1);
-  for (int block = 0; block * kCols * 32 < a.p.D; ++block) {
-    const Columns<kWide> c(block, lane, 32, a.p.D);
-    float acc[kCols] = {};
+  // the parts q0 .. q1 - 1 of the run that begins in piece `from`
+  auto sum = [&](int from, int q0, int q1, float* acc) {
     constexpr int kAhead = 8;
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) acc[k] = 0.f;
     for (int q = q0; q < q1; q += kAhead) {
       Raw<kWide, float> x[kAhead];
 #pragma unroll
       for (int r = 0; r < kAhead; ++r) {
         const int at = min(q + r, q1 - 1);
-        x[r].load(a.part + ((int64_t)(m + at) * 2 + (at == 0)) * a.width + c.at, c);
+        x[r].load(a.part + ((int64_t)(from + at) * 2 + (at == 0)) * a.width + c.at, c);
       }
 #pragma unroll
       for (int r = 0; r < kAhead; ++r) {
@@ -647,18 +644,47 @@ __global__ void __launch_bounds__(kThreads) k_grad_join(SumArgs a, TT* dtable) {
         for (int k = 0; k < kCols; ++k) acc[k] += x[r].get(k);
       }
     }
-#pragma unroll
-    for (int k = 0; k < kCols; ++k) sums[warp][k * 32 + lane] = acc[k];
-    __syncthreads();
-    if (warp == 0) {
-#pragma unroll
-      for (int w = 1; w < kThreads / 32; ++w)
-#pragma unroll
-        for (int k = 0; k < kCols; ++k) acc[k] += sums[w][k * 32 + lane];
-      put_row<kWide>(a.p, dtable, key, c, acc);
+  };
+  float acc[kCols];
+  const int64_t j0 = (int64_t)m * a.piece, j1 = j0 + a.piece;
+  if (j1 < n) {
+    // all looks at once: the piece's borders, and where the pieces after it begin
+    const int64_t ahead = (int64_t)(m + 1 + lane) * a.piece;
+    const int key = __ldg(a.keys + j1), end = __ldg(a.keys + j1 - 1);
+    const int before = j0 > 0 ? __ldg(a.keys + j0 - 1) : -1;
+    const int more = __popc(__ballot_sync(0xffffffffu, ahead < n && __ldg(a.keys + min(ahead, (int64_t)n - 1)) == key));
+    if (key < V && end == key && before != key) {
+      if (more >= kManyParts) {
+        if (lane == 0) long_piece = m;
+      } else {
+        sum(m, 0, more + 1, acc);
+        put_row<kWide>(a.p, dtable, key, c, acc);
+      }
     }
-    __syncthreads();
   }
+  __syncthreads();
+  const int from = long_piece;
+  if (from < 0) return;
+  const int key = __ldg(a.keys + (int64_t)(from + 1) * a.piece);
+  int more = 0;  // pieces after it into which the run goes
+  for (int q0 = from + 1;; q0 += kThreads) {
+    const int64_t q = (int64_t)q0 + threadIdx.x;
+    const int got = __syncthreads_count(q < a.pieces && __ldg(a.keys + q * a.piece) == key);
+    more += got;
+    if (got < kThreads) break;
+  }
+  const int per = (more + 1 + kJoinWarps - 1) / kJoinWarps;
+  const int q0 = min(warp * per, more + 1), q1 = min(q0 + per, more + 1);
+  sum(from, q0, q1, acc);
+#pragma unroll
+  for (int k = 0; k < kCols; ++k) sums[warp][k * 32 + lane] = acc[k];
+  __syncthreads();
+  if (warp != 0) return;
+#pragma unroll
+  for (int w = 1; w < kJoinWarps; ++w)
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) acc[k] += sums[w][k * 32 + lane];
+  put_row<kWide>(a.p, dtable, key, c, acc);
 }
 
 // ---- Host ----------------------------------------------------------------------------------
@@ -754,7 +780,9 @@ cudaError_t grad(const spec_embed_params& p, const int32_t* ids, const TR* drows
                    drows, dtable);
   if (e != cudaSuccess) return e;
   *launches = 3;
-  return launch_after(k_grad_join<kWide, TT>, dim3(g.pieces), kThreads, 0, st, s, dtable);
+  return launch_after(k_grad_join<kWide, TT>,
+                      dim3((g.pieces + kJoinWarps - 1) / kJoinWarps, (p.D + 32 * kCols - 1) / (32 * kCols)),
+                      kThreads, 0, st, s, dtable);
 }
 
 }  // namespace
