@@ -295,8 +295,7 @@ __global__ void __launch_bounds__(32 * kDirectWarps, 2)
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kDigits = 512;                       // 9 bits a pass
-constexpr int kTile = 2048;                        // positions ranked together
-constexpr int kRounds = kTile / kSortThreads;      // of 32 neighbouring positions per warp
+constexpr int kFewRounds = 2, kManyRounds = 4;     // 32 neighbouring positions of a warp each
 static_assert(kDirect <= 65536, "positions of the list fit 16 bits");
 static_assert(kDigits == kSortThreads, "one thread per digit");
 
@@ -307,7 +306,7 @@ struct SortArgs {
   int32_t* pos[2];
   int32_t* hist;      // [CTA][digit]
   int ctas;
-  int per;            // positions per CTA, a multiple of kTile
+  int per;            // positions per CTA, whole tiles
   int passes, bits;   // bits per pass
   uint64_t spin;
   WsHeader* hdr;
@@ -343,8 +342,12 @@ SPEC_DEV int exclusive_scan(int x, int32_t* warps) {
 // 0.3 % of the memory's bandwidth), so a run of one tile (131072 positions) stays
 // in registers, and the counts of all CTAs are requested at once.  Zeroing the
 // table beside it in further CTAs made its barriers slower than it saved (47 us).
+// Up to 65536 positions the tiles are half as long, on as many CTAs (9000: 2 us
+// less; at 131072, where that takes 128 CTAs, 2 us more).
 // Cooperative launch: the CTAs wait for one another.
+template <int kRounds>
 __global__ void __launch_bounds__(kSortThreads) k_grad_sort(SortArgs a) {
+  constexpr int kTile = kRounds * kSortThreads;  // positions ranked together
   __shared__ SortShared sm;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
   const int64_t n = a.p.n, i0 = min((int64_t)cta * a.per, n), i1 = min(i0 + a.per, n);
@@ -691,7 +694,7 @@ __global__ void __launch_bounds__(kThreads) k_grad_join(SumArgs a, TT* dtable) {
 constexpr int kMaxSortCtas = 64;
 
 struct GradPlan {
-  int ctas, per, passes, bits;         // sort
+  int rounds, ctas, per, passes, bits;  // sort
   int piece, pieces, lanes, blocks, width;  // sums
   size_t keys, hist, part, bytes;      // offsets after the two key and position arrays
 };
@@ -700,9 +703,11 @@ size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 
 GradPlan plan_of(const spec_embed_params& p) {
   GradPlan g = {};
-  const int64_t tiles = ((int64_t)p.n + kTile - 1) / kTile;
+  g.rounds = p.n <= kMaxSortCtas * kFewRounds * kSortThreads ? kFewRounds : kManyRounds;
+  const int tile = g.rounds * kSortThreads;
+  const int64_t tiles = ((int64_t)p.n + tile - 1) / tile;
   g.ctas = (int)std::min<int64_t>(tiles, kMaxSortCtas);
-  g.per = (int)((tiles + g.ctas - 1) / g.ctas) * kTile;
+  g.per = (int)((tiles + g.ctas - 1) / g.ctas) * tile;
   g.ctas = (int)(((int64_t)p.n + g.per - 1) / g.per);
   int bits = 1;
   while (bits < 31 && (int64_t(1) << bits) <= p.V) ++bits;  // the largest key is V
@@ -757,8 +762,9 @@ cudaError_t grad(const spec_embed_params& p, const int32_t* ids, const TR* drows
   a.spin = 4000000ull;
   a.hdr = hdr;
   void* args[] = {&a};
-  cudaError_t e = cudaLaunchCooperativeKernel((const void*)k_grad_sort, dim3(g.ctas),
-                                              dim3(kSortThreads), args, 0, st);
+  const void* sort = g.rounds == kFewRounds ? (const void*)k_grad_sort<kFewRounds>
+                                            : (const void*)k_grad_sort<kManyRounds>;
+  cudaError_t e = cudaLaunchCooperativeKernel(sort, dim3(g.ctas), dim3(kSortThreads), args, 0, st);
   if (e != cudaSuccess) return e;
   SumArgs s = {};
   s.p = p;

@@ -68,7 +68,8 @@ def strided(t, extra):
 # lookup and its gradient
 # ---------------------------------------------------------------------------
 EMBED = [(1, 1, 1), (3, 7, 5), (64, 500, 256), (257, 33, 250), (5, 2, 1030), (1000, 3, 64),
-         (4097, 900, 36), (70, 100, 4104), (4096, 1500, 70), (2100, 3000, 256)]
+         (4097, 900, 36), (70, 100, 4104), (4096, 1500, 70), (2100, 3000, 256),
+         (65537, 700, 33), (140000, 1000, 6)]
 
 
 @pytest.mark.parametrize("pad", [0, 3, 8])
