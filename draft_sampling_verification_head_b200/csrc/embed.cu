@@ -195,7 +195,7 @@ SPEC_DEV void zero_rows(const spec_embed_params& p, TT* dtable, int64_t v0, int6
 // Most positions that are not sorted: every CTA looks through all of them, so
 // the direct form's time grows with their square, while the sort's launches and
 // barriers are there from the first on (V 32000, D 256: 1000 positions 14 us,
-// sorted 30; 2048 18 and 33; 4096 29 and 38; 6000 44 and 39).
+// sorted 27; 2048 18 and 33; 4096 29 and 34; 6000 44 and 33).
 constexpr int kDirect = 4096;
 constexpr int kZeroRows = 1024;   // most table rows a CTA zeroes beside them
 
