@@ -458,13 +458,26 @@ __global__ void __launch_bounds__(kSortThreads) k_grad_sort(SortArgs a) {
     }
     if (pass + 1 < a.passes) ok = grid_sync();
   }
-  if (a.ctas > 1 && tid == 0 && ok) {  // the last CTA leaves the counters at zero
+  if (a.ctas == 1) return;
+  // All CTAs are counted, those that gave up in the upper half, and the last one
+  // leaves the counters as the next launch needs them.  After a wait that ran out
+  // the lists are in no order and may hold anything: then no place of them names
+  // a token, so that the launches behind this one read no row and add nothing.
+  bool gave_up = false;
+  if (tid == 0) {
+    if (!ok) report_error(a.hdr, SPEC_ERR_TIMEOUT, SITE_GRID_BARRIER, cta, (int)barrier);
     __threadfence();
-    if (atomicAdd(&a.hdr->exit_count, 1u) == (uint32_t)a.ctas - 1) {
+    const uint32_t left = atomicAdd(&a.hdr->exit_count, ok ? 1u : 0x10001u);
+    if ((left & 0xFFFFu) == (uint32_t)a.ctas - 1) {
+      __threadfence();
+      gave_up = !ok || left >> 16;
       a.hdr->bar = 0;
+      a.hdr->abort = 0;
       a.hdr->exit_count = 0;
     }
   }
+  if (__syncthreads_or(gave_up))
+    for (int64_t i = tid; i < n; i += kSortThreads) a.keys[a.passes & 1][i] = a.p.V;
 }
 
 // ---- Sums of the sorted list -------------------------------------------------------------

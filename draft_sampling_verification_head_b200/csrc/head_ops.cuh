@@ -11,8 +11,8 @@ extern thread_local int32_t g_last_launches;  // kernel launches of the thread's
 int num_sms();                                // SMs of the current device, 0 on an error
 
 // Record a device-side error of an operator: the first one stays.  Unlike
-// record_error this leaves the abort flag alone, which only the persistent
-// kernels of the cycle poll and reset.
+// record_error this leaves the abort flag alone, which ends the waits of the
+// launches that have barriers of the grid (the cycle's, the gradient's sort).
 SPEC_DEV void report_error(WsHeader* h, int32_t code, int32_t site, int32_t a, int32_t b) {
   if (atomicCAS(&h->status, 0, code) == 0) {
     h->err_where = site;

@@ -899,3 +899,34 @@ def test_binding_refuses_what_the_library_cannot_see():
         sd.embed(p, t, ids, torch.zeros(8, 4).cuda().t(), ws)
     with pytest.raises(sd.SpecError):
         sd.embed(p, t, ids, rows, ws[:100])
+
+# ---------------------------------------------------------------------------
+# waits that run out
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("acc", [False, True])
+@pytest.mark.parametrize("n,V,D", [(9000, 50, 12), (70000, 300000, 8)])
+def test_embed_grad_after_a_wait_that_ran_out(n, V, D, acc):
+    """The workspace's abort word, set beforehand, ends the sort's first wait in
+    every CTA.  The launches behind it must not use the lists, which hold
+    anything here: no row is added, the status tells, and the next call on the
+    same workspace is right."""
+    g = gen(11)
+    ids = torch.randint(0, V, (n,), generator=g, dtype=torch.int32).cuda()
+    d, init = rand(g, n, D, dtype="bf16"), rand(g, V, D)
+    p = sd.EmbedParams(n=n, V=V, D=D, dtype="f32", accumulate=acc)
+    want, ws = init.clone(), sd.make_workspace(p)
+    sd.embed_grad(p, ids, d, want, ws)
+    assert sd.sync_status(ws) == sd.SPEC_OK
+    head = ws[:256].view(torch.int32)  # status, three diagnostics, barrier, spare, exits, abort
+    assert bool((head == 0).all())
+    ws[256:] = 0xFF
+    head[7] = 1
+    got = init.clone()
+    sd.embed_grad(p, ids, d, got, ws)
+    assert sd.sync_status(ws) == sd.SPEC_ERR_TIMEOUT
+    assert torch.equal(got, init if acc else torch.zeros_like(init))
+    assert head[4:8].tolist() == [0, 0, 0, 0]
+    head[:4] = 0
+    got = init.clone()
+    sd.embed_grad(p, ids, d, got, ws)
+    assert sd.sync_status(ws) == sd.SPEC_OK and torch.equal(got, want)
