@@ -901,6 +901,112 @@ def test_binding_refuses_what_the_library_cannot_see():
         sd.embed(p, t, ids, rows, ws[:100])
 
 # ---------------------------------------------------------------------------
+# forms that the shapes above do not reach
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("acc", [False, True])
+@pytest.mark.parametrize("pad", [0, 3])
+@pytest.mark.parametrize("dtype,rows", [("f32", "bf16"), ("bf16", "f32")])
+@pytest.mark.parametrize("n,V,D", [
+    # whole warps and several blocks of columns, pieces of 16 to 128 positions
+    (5000, 300, 520), (9000, 700, 1001), (40000, 500, 512), (131072, 2000, 256),
+    # three passes of the sort
+    (5000, 2**18, 4), (9000, 300001, 12),
+    # behind one tile a CTA, and twice that
+    (131073, 1000, 8), (262145, 900, 4)])
+def test_embed_grad_of_many_positions(n, V, D, dtype, rows, pad, acc):
+    g = gen(n + D)
+    ids = (torch.rand(n, generator=g) ** 2 * V).to(torch.int32).clamp_(max=V - 1)
+    ids[torch.rand(n, generator=g) < 0.4] = V // 3  # a run through many pieces
+    ids[n // 2] = -1
+    st, _ = _embed_grad(n, V, D, dtype, rows, pad, acc, ids, g)
+    assert st == sd.SPEC_OK
+
+
+def test_embed_grad_far_rows_of_many_positions(far_buffers):
+    """Row offsets past 2^32 in the sums of the sorted list: dense rows' bits."""
+    a, b = far_buffers
+    n, V, D, stride = 4098, 5, 40, 2**20
+    assert (n - 1) * stride > 2**32 - 1 and n > 4096
+    drows, t = rand(gen(1), n, D, dtype="bf16"), torch.empty(V, D, dtype=torch.bfloat16, device="cuda")
+    ids = torch.randint(0, V, (n,), generator=gen(2), dtype=torch.int32).cuda()
+    p = sd.EmbedParams(n=n, V=V, D=D, table_stride=FAR, row_stride=stride)
+    ws = sd.make_workspace(p)
+    sd.embed_grad(sd.EmbedParams(n=n, V=V, D=D), ids, drows, t, ws)
+    flat, _ = far(a, drows, stride)
+    dtable, got = far(b, torch.ones_like(t), FAR)
+    sd.embed_grad(p, ids, flat, dtable, ws)
+    assert torch.equal(got, t) and sd.sync_status(ws) == sd.SPEC_OK
+    want, mag, count = H.embed_grad(ids.cpu().numpy(), np64(drows), 1.0, np.zeros((V, D)))
+    within(got, want, (count[:, None] + 2) * U * mag + np.abs(want) * half_step("bf16") * (1 + 1e-3))
+
+
+@pytest.mark.parametrize("ragged", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("pad", [0, 2, 8])
+@pytest.mark.parametrize("B,T,D", [(1, 16, 64), (2, 100, 136), (5, 65, 8), (40, 33, 256), (3, 2050, 64),
+                                   # steps split over the GPU
+                                   (1, 6000, 256), (2, 5121, 72),
+                                   # sequences that fill the GPU
+                                   (1200, 40, 128), (300, 70, 192)])
+def test_gated_scan_rows_in_vectors(B, T, D, pad, dtype, ragged):
+    """Widths and strides of whole pairs (2) and of 16 bytes (0, 8)."""
+    gate, x, h0, lens, n = scan_inputs(B, T, D, dtype, B + T + D + pad, ragged)
+    G, X, h064 = clean(gate, n, B, T, D), clean(x, n, B, T, D), np64(h0)
+    gw, xw = strided(gate, pad)[0], strided(x, 2 * pad)[0]
+    h = torch.full((B * T, D + pad), GUARD, dtype=DT[dtype], device="cuda")
+    last = torch.full((B, D), GUARD, device="cuda")
+    states = torch.full((B, -(-T // sd.SPEC_SCAN_CHUNK), D), GUARD, device="cuda")
+    p = sd.ScanParams(B=B, T=T, D=D, dtype=dtype, gate_stride=D + pad, x_stride=D + 2 * pad,
+                      h_stride=D + pad)
+    ws = sd.make_workspace(p)
+    ln = None if lens is None else lens.cuda()
+    sd.gated_scan(p, gw, xw, h0, ln, h, last, states, ws)
+    assert sd.sync_status(ws) == sd.SPEC_OK
+    want, wlast, before, _ = H.gated_scan(G, X, h064, n)
+    err = H.gated_scan_error(G, X, h064, n, STEP)
+    live, hs = np.arange(T)[None, :] < n[:, None], half_step(dtype)
+    hv = np64(h[:, :D]).reshape(B, T, D)
+    within(hv[live], want[live], (err[:, 1:] + np.abs(want) * hs)[live] + TINY, "h")
+    assert np.all(hv[~live] == GUARD) and bool((h[:, D:] == GUARD).all())
+    within(last, wlast, err[:, T] + TINY, "h_last")
+    within(states, before[:, ::sd.SPEC_SCAN_CHUNK], err[:, :T:sd.SPEC_SCAN_CHUNK] + TINY, "states")
+
+    dh, dl = rand(gen(T), B * T, D, dtype=dtype), rand(gen(D), B, D)
+    for b in range(B):
+        dh.view(B, T, D)[b, n[b]:] = float("nan")
+    dg = torch.full((B * T, D + pad), GUARD, dtype=DT[dtype], device="cuda")
+    dx = torch.full((B * T, D + 2 * pad), GUARD, dtype=DT[dtype], device="cuda")
+    d0 = torch.full((B, D), GUARD, device="cuda")
+    sd.gated_scan_grad(p, gw, xw, h0, ln, states, strided(dh, pad)[0], dl, dg, dx, d0, ws)
+    assert sd.sync_status(ws) == sd.SPEC_OK
+    (wg, wx, w0), (eg, ex, e0) = H.gated_scan_grad(G, X, h064, n, np64(dh).reshape(B, T, D),
+                                                   np64(dl), STEP)
+    within(np64(dg[:, :D]).reshape(B, T, D), wg, eg + np.abs(wg) * hs + TINY, "dgate")
+    within(np64(dx[:, :D]).reshape(B, T, D), wx, ex + np.abs(wx) * hs + TINY, "dx")
+    within(d0, w0, e0 + np.abs(w0) * U + TINY, "dh0")
+    assert bool((dg[:, D:] == GUARD).all()) and bool((dx[:, D:] == GUARD).all())
+
+
+@pytest.mark.parametrize("K,V", [(257, 40), (600, 97), (1024, 33)])
+def test_verify_probs_long_blocks(K, V):
+    """More positions than a CTA tests at a time: rejections and bad drafts in
+    every part of the block, lengths that end in any of them."""
+    B = 12
+    t, q, d, ua, ud, g = probs_inputs(B, K, V, "f32", "f32", K, sigma=0.0)
+    q = t[:, :K].clone()
+    d = torch.multinomial(q.reshape(B * K, V), 1, generator=g).view(B, K).to(torch.int32)
+    ua = torch.rand(B, K, generator=g) * 0.99  # all pass, but for:
+    for b, j in enumerate([0, 100, 255, 256, K - 1, K // 2]):
+        t[b, j, d[b, j]] = 0.0
+    d2 = d.clone()
+    d2[6, 256], d2[7, 3] = V, -5
+    assert same_probs(run_probs(t, q, d, ua, ud), t, q, d, ua, ud) == sd.SPEC_OK
+    assert same_probs(run_probs(t, q, d2, ua, ud), t, q, d2, ua, ud) == sd.SPEC_ERR_TOKEN_RANGE
+    kb = np.array([K, K, K, K, K, K, -1, 256, 255, 257, K - 1, 0])
+    assert same_probs(run_probs(t, q, d, ua, ud, kb), t, q, d, ua, ud, kb) == sd.SPEC_OK
+
+
+# ---------------------------------------------------------------------------
 # waits that run out
 # ---------------------------------------------------------------------------
 @pytest.mark.parametrize("acc", [False, True])
