@@ -53,6 +53,7 @@ _SIGS = {
     "spec_verify_probs": (ctypes.c_int, [_P] * 13),
     "spec_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "spec_last_launch_count": (ctypes.c_int32, []),
+    "spec_debug_scan_polls": (ctypes.c_int, [ctypes.c_int64]),
     "spec_debug_philox": (ctypes.c_int, [_P, _P, _P, ctypes.c_int32, _P]),
     "spec_debug_curand_philox": (ctypes.c_int, [_P, _P, _P, ctypes.c_int32, _P]),
 }

@@ -5,6 +5,7 @@
 #include <cstdio>
 
 #include "head_ops.cuh"
+#include "specdec_debug.h"
 
 namespace specdec {
 namespace {
@@ -223,6 +224,11 @@ spec_status spec_gated_scan_grad(const spec_scan_params* p, const void* gate, co
                              (const float*)dh, dh_last, (float*)dgate, (float*)dx, dh0,
                              body_of(ws), header_of(ws), sms, (cudaStream_t)stream, &launches);
   return launched(e, launches);
+}
+
+spec_status spec_debug_scan_polls(int64_t polls) {
+  set_scan_polls(polls);
+  return SPEC_OK;
 }
 
 size_t spec_w4_workspace_size(const spec_w4_params* p) {

@@ -62,6 +62,7 @@ cudaError_t launch_embed_grad(const spec_embed_params& p, const int32_t* ids, co
 
 // ---- Gated linear recurrence and its gradient -------------------------------------
 size_t scan_ws_bytes(const spec_scan_params& p, int num_sms);
+void set_scan_polls(int64_t polls);
 template <typename T>
 cudaError_t launch_scan(const spec_scan_params& p, const T* gate, const T* x, const float* h0,
                         const int32_t* len, T* h, float* h_last, float* states, uint8_t* body,

@@ -21,6 +21,7 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "head_ops.cuh"
@@ -179,6 +180,7 @@ struct ScanArgs {
   int jobs;     // sequences x tiles (x segments)
   int nseg;     // segments per sequence, where a warp has one of its own
   int seg;      // steps per segment, a multiple of kChunk
+  uint64_t polls;  // of a join's wait, until it gives up
   float2* maps;    // [B][nseg][D] a segment's map
   float2* groups;  // [B][nseg / kSoloWarps][D] the map of a CTA's segments
   float* first;    // [B][D] h0 (or dh_last), which the last segment may write over
@@ -264,6 +266,7 @@ struct Joiner<V, 1> {
 };
 
 constexpr uint64_t kJoinPolls = 1ull << 22;  // about 4 s
+std::atomic<int64_t> g_join_polls{-1};       // set by a test; negative: kJoinPolls
 
 template <int V, int W>
 SPEC_DEV void join_init(Joiner<V, W>& sm, int cluster) {
@@ -290,8 +293,8 @@ SPEC_DEV void send(uint32_t to, float2 v, uint32_t bar) {
       "f"(v.x), "f"(v.y), "r"(bar)
       : "memory");
 }
-SPEC_DEV bool cluster_wait(uint64_t* bar, uint32_t parity) {
-  for (uint64_t it = 0; it < kJoinPolls; ++it) {
+SPEC_DEV bool cluster_wait(uint64_t* bar, uint32_t parity, uint64_t polls) {
+  for (uint64_t it = 0; it < polls; ++it) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
@@ -305,9 +308,21 @@ SPEC_DEV bool cluster_wait(uint64_t* bar, uint32_t parity) {
   return false;
 }
 
+// The end of a CTA in which a wait ran out: others may still send to its shared
+// memory, so it stays until their threads have ended or wait here as well (which
+// they do, as their own waits are bounded) and what they sent has arrived.
+SPEC_DEV void cluster_give_up() {
+  cp_async_wait<0>();
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+  __nanosleep(1000000);
+}
+
+// Returns false where the CTA has to leave: a wait of one of its threads ran out
+// in the window before (`ok` of that thread is false).  It sends and arrives no
+// more then, since its barriers' phases are no longer the others'.
 template <int V, int W>
-SPEC_DEV void join(Joiner<V, W>& sm, int win, int warp, int rank, int cluster, Vec<V> a, Vec<V> c,
-                   Vec<V>& carry, Vec<V>& before, WsHeader* hdr) {
+SPEC_DEV bool join(Joiner<V, W>& sm, int win, int warp, int rank, int cluster, Vec<V> a, Vec<V> c,
+                   Vec<V>& carry, Vec<V>& before, bool& ok, uint64_t polls, WsHeader* hdr) {
   const int par = win & 1;
   if constexpr (W == 1) {
     before = carry;
@@ -317,7 +332,10 @@ SPEC_DEV void join(Joiner<V, W>& sm, int win, int warp, int rank, int cluster, V
 #pragma unroll
     for (int v = 0; v < V; ++v)
       sm.piece[par][warp][v * 32 + lane] = make_float2(a.get(v), c.get(v));
-    __syncthreads();
+    if (__syncthreads_or(!ok)) {
+      ok = false;
+      return false;
+    }
     float out_b[V], out_c[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -346,8 +364,8 @@ SPEC_DEV void join(Joiner<V, W>& sm, int win, int warp, int rank, int cluster, V
     if (cluster > 1) {
       if (threadIdx.x == 0)
         mbar_arrive_expect_tx(&sm.full[par], (uint32_t)(cluster * 32 * V * sizeof(float2)));
-      if (!cluster_wait(&sm.full[par], (win >> 1) & 1) && threadIdx.x == 0)
-        report_error(hdr, SPEC_ERR_TIMEOUT, SITE_MBAR_FULL, rank, win);
+      ok = cluster_wait(&sm.full[par], (win >> 1) & 1, polls);
+      if (!ok) report_error(hdr, SPEC_ERR_TIMEOUT, SITE_MBAR_FULL, rank, win);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         float s = carry.get(v), mine = s;
@@ -368,6 +386,7 @@ SPEC_DEV void join(Joiner<V, W>& sm, int win, int warp, int rank, int cluster, V
       carry = {out_c[0]};
     }
   }
+  return true;
 }
 
 template <int V>
@@ -478,6 +497,7 @@ __global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), 2)
     }
   }
   const int nwin = (at.t1 - at.t0 + window - 1) / window;
+  bool ok = true;
   for (int win = 0, stage = 0; win < nwin; ++win, t0 += window) {
     Vec<V> f[kChunk], z[kChunk], ma = Vec<V>::all(1.f), mc = Vec<V>::all(0.f);
     cp_async_wait<kStages - 1>();
@@ -505,7 +525,7 @@ __global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), 2)
     request(t0 + kStages * window, stage);
     stage ^= 1;
     Vec<V> s;
-    join<V, W>(sm.joiner, win, warp, rank, C, ma, mc, carry, s, a.hdr);
+    if (!join<V, W>(sm.joiner, win, warp, rank, C, ma, mc, carry, s, ok, a.polls, a.hdr)) break;
     if (on && a.states && t0 < Tn)
       state_store<V>(a.states + ((int64_t)b * nch + t0 / kChunk) * D + c, s);
     if (on && a.h && left > 0) {
@@ -529,6 +549,7 @@ __global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), 2)
   }
   if (a.h_last && at.pos == a.nseg - 1 && rank == 0 && warp == 0 && on)
     state_store<V>(a.h_last + (int64_t)b * D + c, carry);
+  if (W > 1 && !ok) cluster_give_up();
 }
 
 // Gradient.  The state before each piece comes from `states`, so its h are run
@@ -589,6 +610,7 @@ __global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), 2)
     }
   }
   const int nwin = (ch1 - ch0 + window - 1) / window;
+  bool ok = true;
   for (int win = 0; win < nwin; ++win, ch -= window) {
     const int t0 = ch * kChunk, left = ch < ch0 ? 0 : n - t0, par = win & 1;
     Vec<V> f[kChunk], i[kChunk], w[kChunk], ma = Vec<V>::all(1.f), mc = Vec<V>::all(0.f);
@@ -618,7 +640,7 @@ __global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), 2)
     }
     __syncwarp();
     request(ch - window, par ^ 1);
-    join<V, W>(sm.joiner, win, warp, rank, C, ma, mc, carry, s, a.hdr);
+    if (!join<V, W>(sm.joiner, win, warp, rank, C, ma, mc, carry, s, ok, a.polls, a.hdr)) break;
     if (on && ch >= ch0) {
       T* dg = dgp + (int64_t)t0 * a.p.gate_stride;
       T* dx = dxp + (int64_t)t0 * a.p.x_stride;
@@ -649,6 +671,7 @@ __global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), 2)
   }
   if (a.dh0 && at.pos == a.nseg - 1 && rank == 0 && warp == 0 && on)
     state_store<V>(a.dh0 + (int64_t)b * D + c, carry);
+  if (W > 1 && !ok) cluster_give_up();
 }
 
 // ----------------------------------------------------------------------------
@@ -856,6 +879,8 @@ template <typename T>
 cudaError_t dispatch(ScanArgs& a, bool grad, int num_sms, uint8_t* body, cudaStream_t st,
                      int* launches) {
   a.wide = wide_ok<T>(a);
+  const int64_t polls = g_join_polls.load(std::memory_order_relaxed);
+  a.polls = polls < 0 ? kJoinPolls : (uint64_t)polls;
   if constexpr (std::is_same<T, __nv_bfloat16>::value) {
     if (pairs_ok(a)) return by_shape<T, 2, 8>(a, grad, num_sms, body, st, launches);
   }
@@ -863,6 +888,8 @@ cudaError_t dispatch(ScanArgs& a, bool grad, int num_sms, uint8_t* body, cudaStr
 }
 
 }  // namespace
+
+void set_scan_polls(int64_t polls) { g_join_polls.store(polls); }
 
 size_t scan_ws_bytes(const spec_scan_params& p, int num_sms) {
   size_t need = 0;

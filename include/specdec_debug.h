@@ -1,6 +1,7 @@
 /*
  * specdec debug entry points: expose the random stream so that tests can pin
- * it.  Not needed to run the method.
+ * it, and let waits run out so that tests see what follows.  Not needed to run
+ * the method.
  */
 #ifndef SPECDEC_DEBUG_H
 #define SPECDEC_DEBUG_H
@@ -21,6 +22,11 @@ spec_status spec_debug_philox(const uint32_t *ctr, const uint32_t *key, uint32_t
  * words 0..1), an independent implementation of the published algorithm. */
 spec_status spec_debug_curand_philox(const uint32_t *ctr, const uint32_t *key, uint32_t *out,
                                      int32_t n, spec_stream_t stream);
+
+/* Polls after which a wait between the CTAs of spec_gated_scan and its gradient
+ * gives up, for the launches of this process from now on; 0 gives up at once,
+ * a negative number restores the default (about 4 s). */
+spec_status spec_debug_scan_polls(int64_t polls);
 
 #ifdef __cplusplus
 }

@@ -1036,3 +1036,40 @@ def test_embed_grad_after_a_wait_that_ran_out(n, V, D, acc):
     got = init.clone()
     sd.embed_grad(p, ids, d, got, ws)
     assert sd.sync_status(ws) == sd.SPEC_OK and torch.equal(got, want)
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,T,D", [(5, 200, 72), (2, 2050, 64), (1, 4999, 40)])
+def test_scan_after_waits_that_ran_out(B, T, D, dtype):
+    """Joins between CTAs that give up at once: the call ends, the status tells,
+    nothing outside the outputs is written, and the next call is right."""
+    gate, x, h0, lens, n = scan_inputs(B, T, D, dtype, 3, True, std=1.0)
+    gate, x = torch.nan_to_num(gate), torch.nan_to_num(x)
+    dh, dl = rand(gen(4), B * T, D, dtype=dtype), rand(gen(5), B, D)
+    p = sd.ScanParams(B=B, T=T, D=D, dtype=dtype, h_stride=D + 8)
+    ws, ln = sd.make_workspace(p), lens.cuda()
+
+    def both(states):
+        h = torch.full((B * T, D + 8), GUARD, dtype=DT[dtype], device="cuda")
+        out = [torch.full((B, D), GUARD, device="cuda")]
+        sd.gated_scan(p, gate, x, h0, ln, h, out[0], states, ws)
+        first = sd.sync_status(ws)
+        dg, dx = torch.empty_like(gate), torch.empty_like(x)
+        d0 = torch.empty(B, D, device="cuda")
+        sd.gated_scan_grad(p, gate, x, h0, ln, states, strided(dh, 8)[0], dl, dg, dx, d0, ws)
+        return first, sd.sync_status(ws), h, [out[0], dg, dx, d0]
+
+    states = torch.zeros(B, -(-T // sd.SPEC_SCAN_CHUNK), D, device="cuda")
+    want = both(states)
+    assert want[:2] == (sd.SPEC_OK, sd.SPEC_OK)
+    try:
+        sd._check(sd.lib().spec_debug_scan_polls(0), "spec_debug_scan_polls")
+        gave = both(states.clone())
+    finally:
+        sd.lib().spec_debug_scan_polls(-1)
+    assert gave[:2] == (sd.SPEC_ERR_TIMEOUT, sd.SPEC_ERR_TIMEOUT)
+    late = (torch.arange(T)[None, :] >= torch.from_numpy(n)[:, None]).view(-1).cuda()
+    assert bool((gave[2][late] == GUARD).all()) and bool((gave[2][:, D:] == GUARD).all())
+    sd.workspace_init(ws)
+    again = both(states)
+    assert again[:2] == (sd.SPEC_OK, sd.SPEC_OK) and torch.equal(again[2], want[2])
+    assert all(torch.equal(a, b) for a, b in zip(again[3], want[3]))
