@@ -159,29 +159,34 @@ class Params:
 _DT = {"f32": SPEC_F32, "bf16": SPEC_BF16}
 
 
-class _Held:
-    """What a parameter object's calls need again and again, made once: the
-    objects are frozen.  _c is the C structure, _at its address, _need the
-    workspace size and _args, by call, (name, dtype, rows, row stride, row
-    width) of each tensor, which _ready holds as the call looks at them."""
+class _Calls:
+    """What the calls of one parameter object use: the C structure and its
+    address, by call the (name, dtype, rows, row stride, row width) of each
+    tensor and, as _run looks at them, `ready`; the workspace size `need`, None
+    until it is known."""
+    __slots__ = ("c", "at", "args", "ready", "need")
 
-    def __getattr__(self, name):
-        if name not in ("_c", "_at", "_need", "_args", "_ready"):
-            raise AttributeError(name)
-        c = self._make()
-        for k, v in (("_c", c), ("_at", ctypes.addressof(c)), ("_args", self._tensors()),
-                     ("_ready", {}), ("_need", SPEC_WORKSPACE_MIN)):
-            object.__setattr__(self, k, v)
-        if isinstance(self, EmbedParams):
-            object.__setattr__(self, "_need", int(lib().spec_embed_workspace_size(self._at)))
-        elif isinstance(self, W4Params):
-            object.__setattr__(self, "_need", int(lib().spec_w4_workspace_size(self._at)))
-        elif isinstance(self, ScanParams):
-            object.__setattr__(self, "_need", int(lib().spec_scan_workspace_size(self._at)))
-        return getattr(self, name)
+    def __init__(self, c, args):
+        self.c, self.at, self.args = c, ctypes.addressof(c), args
+        self.ready, self.need = {}, None
+
+
+class _Held:
+    """A parameter object whose calls are prepared once: it is frozen.  The
+    _Calls are made whole and published by one step, which the first of several
+    threads wins, so nobody sees a part of them or another structure's address."""
+
+    def __getattr__(self, name):  # only where the attribute is missing
+        if name != "_calls":
+            raise AttributeError(f"{type(self).__name__!r} object has no attribute {name!r}")
+        return self.__dict__.setdefault("_calls", _Calls(self._make(), self._tensors()))
+
+    def _size(self):
+        """Workspace bytes by the library, 0 where the parameters are invalid."""
+        return SPEC_WORKSPACE_MIN
 
     def c(self):
-        return self._c
+        return self._make()
 
     def __reduce__(self):  # copies make their own C structure
         return type(self), tuple(getattr(self, f.name) for f in fields(self))
@@ -205,6 +210,9 @@ class EmbedParams(_Held):
                                1 if self.accumulate else 0, float(self.scale), 0,
                                self.table_stride, self.row_stride)
 
+    def _size(self):
+        return int(lib().spec_embed_workspace_size(self._calls.at))
+
     def _tensors(self):
         table = (self.dtype, self.V, self.table_stride or self.D, self.D)
         rows = (self.row_dtype, self.n, self.row_stride or self.D, self.D)
@@ -227,6 +235,9 @@ class ScanParams(_Held):
     def _make(self):
         return SpecScanParams(self.B, self.T, self.D, _DT[self.dtype], self.gate_stride,
                               self.x_stride, self.h_stride)
+
+    def _size(self):
+        return int(lib().spec_scan_workspace_size(self._calls.at))
 
     def _tensors(self):
         n, D = self.B * self.T, self.D
@@ -263,6 +274,9 @@ class W4Params(_Held):
         return SpecW4Params(self.B, self.r, self.V, self.group, _DT[self.dtype],
                             _DT[self.scale_dtype], _DT[self.base_dtype], _DT[self.out_dtype],
                             self.x_rows, 0, self.x_stride, self.base_stride, self.out_stride)
+
+    def _size(self):
+        return int(lib().spec_w4_workspace_size(self._calls.at))
 
     def _tensors(self):
         codes, groups = -(-self.r // 128) * 64, self.r // max(self.group, 1)
@@ -319,7 +333,10 @@ def _check(code, what):
 def workspace_size(p) -> int:
     """Bytes of workspace for the calls these parameters (of any kind) belong to."""
     if isinstance(p, _Held):
-        return p._need
+        need = p._calls.need
+        if need is None:
+            need = p._calls.need = p._size()
+        return need
     return int(lib().spec_workspace_size(ctypes.byref(p.c())))
 
 
@@ -487,13 +504,13 @@ def _check_rows(name, t, rows, stride, width):
         apart *= t.size(k)
 
 
-def _typed(p, call):
+def _typed(held, call):
     """The tensors of a call as _run looks at them: (torch dtype, row stride,
     elements of all rows), and what _check_rows wants."""
     types = (_TORCH or _torch())[2]
     args = tuple((types[dt], stride, rows * stride, name, dt, rows, width)
-                 for name, dt, rows, stride, width in p._args[call])
-    p._ready[call] = args
+                 for name, dt, rows, stride, width in held.args[call])
+    held.ready[call] = args
     return args
 
 
@@ -501,6 +518,7 @@ def _run(fn, p, call, tensors, ws, stream):
     """One operator's call, after the checks that the C side cannot make.
     Tensors, workspace and stream must belong to the current device."""
     current, raw, _ = _TORCH or _torch()
+    held = p._calls
     dev = current()
     if stream is None:
         st = raw(dev)
@@ -509,8 +527,8 @@ def _run(fn, p, call, tensors, ws, stream):
     else:
         raise ValueError("the stream belongs to another device than the current one")
     ptr = []
-    for t, (dtype, stride, total, name, dt, rows, width) in zip(tensors, p._ready.get(call)
-                                                                or _typed(p, call)):
+    for t, (dtype, stride, total, name, dt, rows, width) in zip(tensors, held.ready.get(call)
+                                                                or _typed(held, call)):
         if t is None:
             ptr.append(None)
             continue
@@ -522,9 +540,9 @@ def _run(fn, p, call, tensors, ws, stream):
         if not (t.is_contiguous() and t.numel() >= total and t.size(-1) == stride):
             _check_rows(name, t, rows, stride, width)
         ptr.append(t.data_ptr())
-    if ws.get_device() != dev or ws.nbytes < p._need:
+    if ws.get_device() != dev or ws.nbytes < workspace_size(p):
         raise SpecError(SPEC_ERR_WORKSPACE, f"{fn}: workspace too small or on another device")
-    code = getattr(_lib or lib(), fn)(p._at, *ptr, ws.data_ptr(), st)
+    code = getattr(_lib or lib(), fn)(held.at, *ptr, ws.data_ptr(), st)
     if code != SPEC_OK:
         raise SpecError(code, fn)
 
@@ -575,7 +593,7 @@ def w4_quantize(p: W4Params, W, stream=None):
         wq = torch.empty(p.V, -(-p.r // 128) * 64, dtype=torch.uint8, device=W.device)
         wscale = torch.empty(p.V, p.r // p.group, device=W.device,
                              dtype=torch.bfloat16 if p.scale_dtype == "bf16" else torch.float32)
-    _check(lib().spec_w4_quantize(p._at, W.data_ptr(), SPEC_BF16 if W.dtype is torch.bfloat16
+    _check(lib().spec_w4_quantize(p._calls.at, W.data_ptr(), SPEC_BF16 if W.dtype is torch.bfloat16
                                   else SPEC_F32, wq.data_ptr(), wscale.data_ptr(),
                                   s.cuda_stream), "spec_w4_quantize")
     return wq, wscale

@@ -316,3 +316,89 @@ def test_parameter_objects_copy_with_a_structure_of_their_own():
     assert p.c().V == 10
     for q in (copy.copy(p), copy.deepcopy(p), pickle.loads(pickle.dumps(p))):
         assert q == p and q.c() is not p.c() and q.c().V == 10
+
+
+# ---- parameter objects used by several threads ---------------------------------------
+class _SlowLibrary:
+    """The library, whose first workspace size is asked for takes until `go`."""
+
+    def __init__(self, real):
+        import threading
+        self.real, self.asked, self.go, self.first = real, threading.Event(), threading.Event(), True
+
+    def __getattr__(self, name):
+        f = getattr(self.real, name)
+        if not name.endswith("_workspace_size"):
+            return f
+
+        def size(p):
+            if self.first:
+                self.first = False
+                self.asked.set()
+                assert self.go.wait(20)
+            return f(p)
+        return size
+
+
+def test_threads_see_a_parameter_object_whole(monkeypatch):
+    """While one thread still asks for the size, another gets the true one, and
+    both keep the address of one structure."""
+    import threading
+    want = sd.workspace_size(sd.EmbedParams(n=200000, V=32000, D=256))
+    assert want > sd.SPEC_WORKSPACE_MIN
+    slow = _SlowLibrary(sd.lib())
+    monkeypatch.setattr(sd, "_lib", slow)
+    p, got = sd.EmbedParams(n=200000, V=32000, D=256), []
+    t = threading.Thread(target=lambda: got.append(sd.workspace_size(p)))
+    t.start()
+    assert slow.asked.wait(20)
+    try:
+        assert sd.workspace_size(p) == want
+    finally:
+        slow.go.set()
+        t.join()
+    assert got == [want] and sd.workspace_size(p) == want
+    assert p._calls.at == ctypes.addressof(p._calls.c)
+
+
+def test_many_threads_ask_a_fresh_parameter_object():
+    import sys
+    import threading
+    every = sys.getswitchinterval()
+    sys.setswitchinterval(1e-6)
+    try:
+        want = sd.workspace_size(sd.EmbedParams(n=50000, V=1000, D=64))
+        for _ in range(200):
+            p, got, gate = sd.EmbedParams(n=50000, V=1000, D=64), [], threading.Barrier(3)
+
+            def ask():
+                gate.wait()
+                got.append((sd.workspace_size(p), p._calls.at))
+            ts = [threading.Thread(target=ask) for _ in range(3)]
+            for t in ts:
+                t.start()
+            for t in ts:
+                t.join()
+            assert got == [(want, ctypes.addressof(p._calls.c))] * 3
+    finally:
+        sys.setswitchinterval(every)
+
+
+def test_a_library_that_is_missing_at_first_leaves_nothing_behind(monkeypatch):
+    p = sd.EmbedParams(n=50000, V=1000, D=64)
+    real = sd.lib()
+
+    def fails(*_):
+        raise RuntimeError("not built")
+    with monkeypatch.context() as m:
+        m.setattr(sd, "lib", fails)
+        with pytest.raises(RuntimeError):
+            sd.workspace_size(p)
+    assert sd.workspace_size(p) == real.spec_embed_workspace_size(ctypes.byref(p.c()))
+
+
+def test_a_changed_copy_of_the_structure_changes_no_call():
+    p = sd.EmbedParams(n=50000, V=1000, D=64)
+    need = sd.workspace_size(p)
+    p.c().n = 2**29
+    assert p.c().n == 50000 and sd.lib().spec_embed_workspace_size(p._calls.at) == need
