@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from contextlib import nullcontext
 from dataclasses import dataclass, fields
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -162,13 +163,13 @@ _DT = {"f32": SPEC_F32, "bf16": SPEC_BF16}
 class _Calls:
     """What the calls of one parameter object use: the C structure and its
     address, by call the (name, dtype, rows, row stride, row width) of each
-    tensor and, as _run looks at them, `ready`; the workspace size `need`, None
-    until it is known."""
+    tensor and, as _run looks at them, `ready`; and by device the workspace
+    sizes `need` that are known."""
     __slots__ = ("c", "at", "args", "ready", "need")
 
     def __init__(self, c, args):
         self.c, self.at, self.args = c, ctypes.addressof(c), args
-        self.ready, self.need = {}, None
+        self.ready, self.need = {}, {}
 
 
 class _Held:
@@ -182,7 +183,8 @@ class _Held:
         return self.__dict__.setdefault("_calls", _Calls(self._make(), self._tensors()))
 
     def _size(self):
-        """Workspace bytes by the library, 0 where the parameters are invalid."""
+        """Workspace bytes by the library on the current device; 0 where the
+        parameters are invalid (or, for the recurrence, without a GPU)."""
         return SPEC_WORKSPACE_MIN
 
     def c(self):
@@ -331,25 +333,26 @@ def _check(code, what):
 
 
 def workspace_size(p) -> int:
-    """Bytes of workspace for the calls these parameters (of any kind) belong to."""
+    """Bytes of workspace for the calls these parameters (of any kind) belong to,
+    on the current device."""
     if isinstance(p, _Held):
-        need = p._calls.need
-        if need is None:
-            need = p._calls.need = p._size()
-        return need
+        return p._size()
     return int(lib().spec_workspace_size(ctypes.byref(p.c())))
 
 
 def make_workspace(p, device="cuda"):
     """Allocate and zero a workspace for these parameters (torch memory)."""
     import torch
-    n = workspace_size(p)
-    if n == 0:
-        raise SpecError(SPEC_ERR_INVALID_ARG, "spec_workspace_size")
-    ws = torch.empty(n + 256, dtype=torch.uint8, device=device)
-    off = (-ws.data_ptr()) % 256
-    ws = ws[off:off + n]
-    _check(lib().spec_workspace_init(_ptr(ws), n, _stream(None)), "spec_workspace_init")
+    d = torch.device(device)
+    named = d.type == "cuda" and d.index is not None
+    with torch.cuda.device(d) if named else nullcontext():  # sized for it, zeroed on its stream
+        n = workspace_size(p)
+        if n == 0:
+            raise SpecError(SPEC_ERR_INVALID_ARG, "spec_workspace_size")
+        ws = torch.empty(n + 256, dtype=torch.uint8, device=device)
+        off = (-ws.data_ptr()) % 256
+        ws = ws[off:off + n]
+        _check(lib().spec_workspace_init(_ptr(ws), n, _stream(None)), "spec_workspace_init")
     return ws
 
 
@@ -504,6 +507,16 @@ def _check_rows(name, t, rows, stride, width):
         apart *= t.size(k)
 
 
+def _need(p, dev):
+    """Workspace bytes that a call on `dev`, the current device, needs.  The
+    recurrence splits its steps by the device's size, so each has its own; a 0
+    (no device, bad parameters: the library says which) is asked for again."""
+    need = p._size()
+    if need > 0:
+        p._calls.need[dev] = need
+    return need
+
+
 def _typed(held, call):
     """The tensors of a call as _run looks at them: (torch dtype, row stride,
     elements of all rows), and what _check_rows wants."""
@@ -540,7 +553,7 @@ def _run(fn, p, call, tensors, ws, stream):
         if not (t.is_contiguous() and t.numel() >= total and t.size(-1) == stride):
             _check_rows(name, t, rows, stride, width)
         ptr.append(t.data_ptr())
-    if ws.get_device() != dev or ws.nbytes < workspace_size(p):
+    if ws.get_device() != dev or ws.nbytes < (held.need.get(dev) or _need(p, dev)):
         raise SpecError(SPEC_ERR_WORKSPACE, f"{fn}: workspace too small or on another device")
     code = getattr(_lib or lib(), fn)(held.at, *ptr, ws.data_ptr(), st)
     if code != SPEC_OK:

@@ -402,3 +402,22 @@ def test_a_changed_copy_of_the_structure_changes_no_call():
     need = sd.workspace_size(p)
     p.c().n = 2**29
     assert p.c().n == 50000 and sd.lib().spec_embed_workspace_size(p._calls.at) == need
+
+
+# ---- workspace sizes by device --------------------------------------------------------
+def test_workspace_sizes_belong_to_a_device(monkeypatch):
+    """The recurrence's scratch grows with the device's multiprocessors, and is
+    unknown without one: what one device needs is not taken for another's."""
+    p = sd.ScanParams(B=1, T=60000, D=64)
+    now, sizes = [0], {0: 0, 1: 5000, 2: 9000}
+    monkeypatch.setattr(sd.ScanParams, "_size", lambda self: sizes[now[0]])
+
+    def need(dev):  # as the calls look it up
+        return p._calls.need.get(dev) or sd._need(p, dev)
+
+    assert sd.workspace_size(p) == 0 and need(0) == 0
+    sizes[0] = 7000  # a device has come up since
+    assert sd.workspace_size(p) == 7000 and need(0) == 7000
+    for dev in (1, 2, 0, 1):
+        now[0] = dev
+        assert need(dev) == sizes[dev] == sd.workspace_size(p)
