@@ -507,6 +507,9 @@ def _check_rows(name, t, rows, stride, width):
         apart *= t.size(k)
 
 
+_STATUS_ONLY = frozenset(("embed", "verify"))  # calls without scratch: any workspace will do
+
+
 def _need(p, dev):
     """Workspace bytes that a call on `dev`, the current device, needs.  The
     recurrence splits its steps by the device's size, so each has its own; a 0
@@ -553,7 +556,8 @@ def _run(fn, p, call, tensors, ws, stream):
         if not (t.is_contiguous() and t.numel() >= total and t.size(-1) == stride):
             _check_rows(name, t, rows, stride, width)
         ptr.append(t.data_ptr())
-    if ws.get_device() != dev or ws.nbytes < (held.need.get(dev) or _need(p, dev)):
+    need = SPEC_WORKSPACE_MIN if call in _STATUS_ONLY else held.need.get(dev) or _need(p, dev)
+    if ws.get_device() != dev or ws.nbytes < need:
         raise SpecError(SPEC_ERR_WORKSPACE, f"{fn}: workspace too small or on another device")
     code = getattr(_lib or lib(), fn)(held.at, *ptr, ws.data_ptr(), st)
     if code != SPEC_OK:

@@ -1073,3 +1073,24 @@ def test_scan_after_waits_that_ran_out(B, T, D, dtype):
     again = both(states)
     assert again[:2] == (sd.SPEC_OK, sd.SPEC_OK) and torch.equal(again[2], want[2])
     assert all(torch.equal(a, b) for a, b in zip(again[3], want[3]))
+
+
+def test_calls_without_scratch_take_any_workspace():
+    """The lookup of many rows and the verification on the smallest workspace and
+    on another operator's; the gradient refuses them."""
+    n, V, D = 9000, 300, 24
+    g = gen(15)
+    t, ids = rand(g, V, D), torch.randint(0, V, (n,), generator=g, dtype=torch.int32).cuda()
+    p = sd.EmbedParams(n=n, V=V, D=D, dtype="f32", row_dtype="f32")
+    pr, q, d, ua, ud, _ = (v.cuda() if isinstance(v, torch.Tensor) else v
+                           for v in probs_inputs(3, 2, 500, "f32", "f32", 7))
+    pp = sd.ProbsParams(B=3, K=2, V=500)
+    for other in (pp, sd.ScanParams(B=2, T=3, D=4), sd.W4Params(B=1, r=32, V=8, group=32)):
+        ws, rows = sd.make_workspace(other), torch.empty(n, D, device="cuda")
+        assert sd.workspace_size(p) > ws.numel()
+        sd.embed(p, t, ids, rows, ws)
+        out, tau = torch.empty(3, 3, dtype=torch.int32).cuda(), torch.empty(3, dtype=torch.int32).cuda()
+        sd.verify_probs(pp, pr, q, d, ua, ud, None, out, tau, None, None, ws)
+        assert sd.sync_status(ws) == sd.SPEC_OK and torch.equal(rows, t[ids.long()])
+        with pytest.raises(sd.SpecError):
+            sd.embed_grad(p, ids, rows, t, ws)
