@@ -122,8 +122,9 @@ SPEC_DEV void raw_store(T* p, Vec<V> x) {
 }
 
 // f = sigmoid(g) = 1 / (1 + e), i = 1 - f = e f with e = exp(-g), so neither is
-// found by cancellation.  g is clamped to [-87, 100], where e stays a number
-// and f, i are 0 and 1 to fp32's range; a NaN passes.  e = 2^t (1 + d) where t
+// found by cancellation.  g is clamped to [-87, 87], where e, f and i stay normal
+// numbers above 0: nothing in fp32's range is lost by it, and an infinite state or
+// input stays infinite; a NaN passes.  e = 2^t (1 + d) where t
 // is -g log2(e) rounded to fp32 and d makes up for that rounding, which for
 // large |g| would cost more than the rest together.
 template <typename T, int V>
@@ -133,7 +134,7 @@ SPEC_DEV void gate_of(RawOf<T, V> raw, Vec<V>& f, Vec<V>& i) {
   if constexpr (std::is_same<T, float>::value) {
     float g = __uint_as_float(raw);
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(g) : "f"(g), "f"(-87.f));
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(g) : "f"(g), "f"(100.f));
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(g) : "f"(g), "f"(87.f));
     constexpr float kL = 1.44269504089f;
     t.v = g * -kL;
     d.v = fmaf(g, -kL, -t.v) * kLn2;
@@ -144,7 +145,7 @@ SPEC_DEV void gate_of(RawOf<T, V> raw, Vec<V>& f, Vec<V>& i) {
     constexpr float kLo = (float)(1.4426950408889634 - 47274.0 / 32768.0);
     uint32_t g2 = raw;
     asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(g2) : "r"(g2), "r"(0xC2AEC2AEu));  // -87
-    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(g2) : "r"(g2), "r"(0x42C842C8u));  // 100
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(g2) : "r"(g2), "r"(0x42AE42AEu));  // 87
     const Vec<V> g = raw_value<T, V>((RawOf<T, V>)g2);
     t = g * Vec<V>::all(-kHi);
     d = g * Vec<V>::all(-kLo * kLn2);
@@ -158,6 +159,11 @@ SPEC_DEV void gate_of(RawOf<T, V> raw, Vec<V>& f, Vec<V>& i) {
   });
   i = e * f;
 }
+
+// A product of gates is above 0, however many: where it leaves fp32's range it is
+// held at the smallest normal number, so that an infinite state times it stays
+// infinite.  A finite state s gains less than s 2^-126 by it.
+SPEC_DEV float above_zero(float product) { return fmaxf(product, 1.17549435e-38f); }
 
 struct ScanArgs {
   spec_scan_params p;
@@ -350,6 +356,8 @@ SPEC_DEV bool join(Joiner<V, W>& sm, int win, int warp, int rank, int cluster, V
         ta *= m.x;
         tc = fmaf(m.x, tc, m.y);
       }
+      ta = above_zero(ta);
+      pa = above_zero(pa);
       if (cluster > 1) {
         if (warp < cluster)  // the warps hand the CTA's map to one CTA each
           send(at_rank(smem_u32(&sm.cta[par][rank][v * 32 + lane]), warp), make_float2(ta, tc),
@@ -428,7 +436,7 @@ SPEC_DEV Vec<V> segment_start(const ScanArgs& a, Joiner<V, 1>& sm, const Place& 
       ma *= m.x;
       mc = fmaf(m.x, mc, m.y);
     }
-    sm.part[wid][v * 32 + lane] = make_float2(ma, mc);
+    sm.part[wid][v * 32 + lane] = make_float2(above_zero(ma), mc);
     __syncthreads();
     s[v] = on ? __ldcg(a.first + (int64_t)at.b * D + c + v) : 0.f;
 #pragma unroll
@@ -521,6 +529,7 @@ __global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), 2)
       ma = ma * f[k];
       mc = fma(f[k], mc, z[k]);
     }
+    ma = ma.map(above_zero);
     __syncwarp();
     request(t0 + kStages * window, stage);
     stage ^= 1;
@@ -638,6 +647,7 @@ __global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), 2)
       ma = ma * f[k];
       mc = f[k] * (mc + raw_value<T, V>(sm.dh[par][wid].at[k][lane]));
     }
+    ma = ma.map(above_zero);
     __syncwarp();
     request(ch - window, par ^ 1);
     if (!join<V, W>(sm.joiner, win, warp, rank, C, ma, mc, carry, s, ok, a.polls, a.hdr)) break;
@@ -739,7 +749,7 @@ __global__ void __launch_bounds__(32 * kSoloWarps, 2) k_scan_maps(ScanArgs a) {
   }
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const float2 m = make_float2(ma.get(v), mc.get(v));
+    const float2 m = make_float2(above_zero(ma.get(v)), mc.get(v));
     sm.part[wid][v * 32 + lane] = m;
     if (at.pos == 0 && c < D) {
       const float* first = kGrad ? a.dh_last : a.h0;
@@ -758,7 +768,7 @@ __global__ void __launch_bounds__(32 * kSoloWarps, 2) k_scan_maps(ScanArgs a) {
       tc = fmaf(m.x, tc, m.y);
     }
     a.groups[((int64_t)b * (a.nseg / kSoloWarps) + at.pos / kSoloWarps) * D + c + wid] =
-        make_float2(ta, tc);
+        make_float2(above_zero(ta), tc);
   }
 }
 

@@ -374,7 +374,9 @@ size_t spec_scan_workspace_size(const spec_scan_params *p);
  *   states   [B, ceil(T / SPEC_SCAN_CHUNK), D] float, or NULL: the state before
  *            every SPEC_SCAN_CHUNK-th step, which the gradient needs (past the
  *            end of a sequence: its last state)
- * States are carried in fp32. */
+ * States are carried in fp32.  Gates beyond -87 and 87, and products of gates
+ * below 2^-126, count as these: an infinite state or input stays infinite, as
+ * in the formula. */
 spec_status spec_gated_scan(const spec_scan_params *p, const void *gate, const void *x,
                             const float *h0, const int32_t *len, void *h, float *h_last,
                             float *states, void *workspace, spec_stream_t stream);

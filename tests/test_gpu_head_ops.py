@@ -1094,3 +1094,66 @@ def test_calls_without_scratch_take_any_workspace():
         assert sd.sync_status(ws) == sd.SPEC_OK and torch.equal(rows, t[ids.long()])
         with pytest.raises(sd.SpecError):
             sd.embed_grad(p, ids, rows, t, ws)
+
+
+def like_definition(got, want, tol, what):
+    """The same NaN and infinities, and finite values within tol."""
+    got = np64(got) if isinstance(got, torch.Tensor) else got
+    for f in (np.isnan, np.isposinf, np.isneginf):
+        assert np.array_equal(f(got), f(want)), (what, f.__name__, np.argwhere(f(got) != f(want))[:4])
+    fin = np.isfinite(want)
+    within(got[fin], want[fin], tol[fin], what)
+
+
+@pytest.mark.parametrize("std", [2.0, 30.0])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,T,D", [(2, 16, 64), (2, 500, 64), (2, 2050, 40), (1, 6000, 64), (2, 6001, 33),
+                                   (1200, 60, 66)])
+def test_scan_infinities_stay(B, T, D, dtype, std):
+    """Infinite states, inputs and gradients over hundreds of steps, after which
+    the product of the gates is below any fp32 number, and NaN beside them."""
+    gate, x, h0, _, n = scan_inputs(B, T, D, dtype, 77, False, std=std)
+    inf, nan, mid = float("inf"), float("nan"), T // 3
+    xv, gv = x.view(B, T, D), gate.view(B, T, D)
+    h0[:, 0], h0[:, 1] = inf, -inf
+    xv[:, mid, 2], xv[:, 3, 3], xv[:, T - 2, 3] = inf, -inf, inf  # channel 3 ends in NaN
+    xv[:, mid, 4], gv[:, mid + 1, 5] = nan, nan
+    gv[:, ::2, 6], gv[:, 1::2, 6], gv[:, :, 7], gv[:, :, 8] = 300.0, -300.0, 200.0, -200.0
+    xv[:, 5, 6], xv[:, 5, 7], xv[:, 5, 8] = inf, -inf, inf
+    dh, dl = rand(gen(1), B, T, D, dtype=dtype), rand(gen(2), B, D)
+    # what infinities are multiplied by keeps its sign whatever the rounding: delta
+    # of the infinite states, and h_{t-1} - x_t (h is a mean of smaller inputs)
+    dh[..., :9], dl[:, :9] = dh[..., :9].abs() + 0.5, dl[:, :9].abs() + 0.5
+    xv[..., 9:13] = torch.exp2(torch.arange(1, T + 1) * (60.0 / T)).to(xv)[:, None]
+    h0[:, 9:13] = 0.0
+    dl[:, 9], dl[:, 10] = inf, nan
+    dh[:, T // 2, 11], dh[:, T - 1, 12], dh[:, 2, 12] = -inf, inf, -inf
+    G, X, h064 = clean(gate, n, B, T, D), clean(x, n, B, T, D), np64(h0)
+    # Gates count as held in -87 .. 87: that moves f and 1 - f by up to e^-87 = 1.6e-38
+    # and a result by that times the inputs, which are up to 2^60 here, so TINY, made
+    # for inputs around 1, does not hold it; the definition is taken of the held gates.
+    G = np.clip(G, -87.0, 87.0)
+    p = sd.ScanParams(B=B, T=T, D=D, dtype=dtype)
+    ws = sd.make_workspace(p)
+    h, last = torch.empty(B, T, D, dtype=DT[dtype], device="cuda"), torch.empty(B, D, device="cuda")
+    states = torch.empty(B, -(-T // sd.SPEC_SCAN_CHUNK), D, device="cuda")
+    sd.gated_scan(p, gate, x, h0, None, h, last, states, ws)
+    dg, dx, d0 = torch.empty_like(h), torch.empty_like(h), torch.empty_like(last)
+    sd.gated_scan_grad(p, gate, x, h0, None, states, dh, dl, dg, dx, d0, ws)
+    assert sd.sync_status(ws) == sd.SPEC_OK
+    hs = half_step(dtype)
+    with np.errstate(all="ignore"):
+        want, wlast, before, _ = H.gated_scan(G, X, h064, n)
+        err = H.gated_scan_error(G, X, h064, n, STEP)
+        (wg, wx, w0), (eg, ex, e0) = H.gated_scan_grad(G, X, h064, n, np64(dh), np64(dl), STEP)
+        like_definition(h, want, err[:, 1:] + np.abs(want) * hs + TINY, "h")
+        like_definition(last, wlast, err[:, T] + TINY, "h_last")
+        like_definition(states, before[:, ::sd.SPEC_SCAN_CHUNK], err[:, :T:sd.SPEC_SCAN_CHUNK] + TINY, "states")
+        like_definition(dx, wx, ex + np.abs(wx) * hs + TINY, "dx")
+        # an infinite delta times h_{t-1} - x_t: where two bf16 inputs in a row are equal
+        # and the gate is saturated, that difference is smaller than its error, which
+        # is h's bound and the subtraction's rounding, so it may be 0 or of either sign
+        known = ~(np.isinf(wx) & (np.abs(before - X) <= err[:, :T] + U * (np.abs(before) + np.abs(X))))
+        assert known.mean() > 0.99
+        like_definition(np64(dg)[known], wg[known], (eg + np.abs(wg) * hs + TINY)[known], "dgate")
+        like_definition(d0, w0, e0 + np.abs(w0) * U + TINY, "dh0")
