@@ -1,6 +1,7 @@
 // Vocabulary product with 4-bit weights and group scales, and the quantiser
 // that lays a factor out for it.
 #include <algorithm>
+#include <cfloat>
 
 #include "head_ops.cuh"
 
@@ -344,8 +345,10 @@ __global__ void __launch_bounds__(kThreads)
   uint32_t words[16];
   const int ng = p.r / p.group;
   auto at = [&](int k) {
+    // an infinity counts as the largest number of its sign: the scale stays finite,
+    // where inf / inf would give NaN and a finite weight's code no meaning
     const float w = load_f(W, (int64_t)k * p.V + v);
-    return w == w ? w : 0.f;
+    return w == w ? fminf(fmaxf(w, -FLT_MAX), FLT_MAX) : 0.f;
   };
   float scale = 0.f;
 #pragma unroll
@@ -363,7 +366,7 @@ __global__ void __launch_bounds__(kThreads)
       }
       word = 0;
       for (int j = 0; j < 8; ++j) {
-        // the clamp on the quotient also takes the infinities
+        // a scale rounded down can leave the largest weights past the codes' ends
         const float q = scale > 0.f ? rintf(fminf(fmaxf(at(k0 + j) / scale, -8.f), 7.f)) : 0.f;
         word |= (uint32_t)((int)q + 8) << (4 * j);
       }

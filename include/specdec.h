@@ -437,8 +437,8 @@ spec_status spec_bias_w4(const spec_w4_params *p, const void *x, const int32_t *
 /* Lay a factor W [r, V] (dtype w_dtype, as for spec_markov_bias) out for
  * spec_bias_w4: per token and group, scale = max |W| / 7 rounded to
  * scale_dtype, code = 8 + W / scale rounded to nearest even and clamped to
- * 0..15 (8 where the scale is 0; a NaN counts as 0).  Uses r, V, group and
- * scale_dtype of p.  wq and wscale are outputs of the sizes above. */
+ * 0..15 (8 where the scale is 0).  A NaN counts as 0, an infinity as the largest
+ * finite float of its sign.  Uses r, V, group and scale_dtype of p.  wq and wscale are outputs of the sizes above. */
 spec_status spec_w4_quantize(const spec_w4_params *p, const void *W, int32_t w_dtype, void *wq,
                              void *wscale, spec_stream_t stream);
 

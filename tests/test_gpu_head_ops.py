@@ -1157,3 +1157,30 @@ def test_scan_infinities_stay(B, T, D, dtype, std):
         assert known.mean() > 0.99
         like_definition(np64(dg)[known], wg[known], (eg + np.abs(wg) * hs + TINY)[known], "dgate")
         like_definition(d0, w0, e0 + np.abs(w0) * U + TINY, "dh0")
+
+
+@pytest.mark.parametrize("wd", ["f32", "bf16"])
+@pytest.mark.parametrize("sdt", ["f32", "bf16"])
+def test_w4_quantize_infinities_and_nan(sdt, wd):
+    """An infinite weight takes the code of its sign under the largest scale, a NaN
+    the code of 0; the other groups and tokens are as without them."""
+    r, V, group = 128, 40, 32
+    W = rand(gen(8), r, V, dtype=wd, std=0.02)
+    p = sd.W4Params(B=1, r=r, V=V, group=group, scale_dtype=sdt)
+    wq0, s0 = sd.w4_quantize(p, W)
+    inf = float("inf")
+    W[3, 0], W[70, 1], W[40, 2], W[41, 2], W[5, 3] = inf, -inf, inf, -inf, float("nan")
+    wq, s = sd.w4_quantize(p, W)
+    codes, was = H.w4_unpack(wq.cpu().numpy(), r), H.w4_unpack(wq0.cpu().numpy(), r)
+    top = np64(torch.tensor(torch.finfo(torch.float32).max / 7).to(DT[sdt]))
+    want, ws = was.copy(), np64(s0)
+    for v, part in ((0, 0), (1, 2), (2, 1)):
+        want[v, part * group:(part + 1) * group], ws[v, part] = 8, top
+    want[0, 3], want[1, 70], want[2, 40], want[2, 41] = 15, 1, 15, 1
+    assert np.array_equal(codes[:3], want[:3])
+    # fp32's largest number through 7: the division's and the type's rounding
+    within(np64(s)[:3], ws[:3], ws[:3] * (half_step(sdt) + 2 * U))
+    W[5, 3] = 0.0
+    wqn, sn = sd.w4_quantize(p, W)
+    assert torch.equal(wq[3:], wqn[3:]) and torch.equal(s[3:], sn[3:]) and codes[3, 5] == 8
+    assert torch.equal(wq[4:], wq0[4:]) and torch.equal(s[4:], s0[4:]) and bool(torch.isfinite(s).all())
