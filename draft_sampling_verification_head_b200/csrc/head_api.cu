@@ -177,8 +177,8 @@ spec_status spec_gated_scan(const spec_scan_params* p, const void* gate, const v
   const spec_status s = check_scan(p, &d);
   if (s != SPEC_OK) return s;
   if (!good_workspace(ws)) return SPEC_ERR_WORKSPACE;
-  if (!h && !h_last && !states) return SPEC_ERR_INVALID_ARG;
-  if (d.T > 0 && (!gate || !x)) return SPEC_ERR_INVALID_ARG;
+  // no steps: h and states have no element, so their pointers may be NULL
+  if (d.T > 0 && (!gate || !x || (!h && !h_last && !states))) return SPEC_ERR_INVALID_ARG;
   if (!aligned_to(gate, d.dtype) || !aligned_to(x, d.dtype) || !aligned_to(h, d.dtype) ||
       !aligned4(h0) || !aligned4(h_last) || !aligned4(states) || !aligned4(len))
     return SPEC_ERR_INVALID_ARG;

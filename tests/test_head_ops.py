@@ -421,3 +421,14 @@ def test_workspace_sizes_belong_to_a_device(monkeypatch):
     for dev in (1, 2, 0, 1):
         now[0] = dev
         assert need(dev) == sizes[dev] == sd.workspace_size(p)
+
+
+# ---- sequences without steps ------------------------------------------------------------
+def test_scan_without_steps_and_without_a_last_state():
+    """h [B, 0, D] and the states are empty, and empty tensors lie at address 0: no
+    work, as for the gradient, and no missing output."""
+    none = [None] * 7
+    assert _call("spec_gated_scan", _scan(T=0), *none, FAKE, None) == sd.SPEC_OK
+    assert sd.last_launch_count() == 0
+    assert _call("spec_gated_scan", _scan(T=1), FAKE, FAKE, *none[2:], FAKE, None) == sd.SPEC_ERR_INVALID_ARG
+    assert _call("spec_gated_scan", _scan(T=0), *none, None, None) == sd.SPEC_ERR_WORKSPACE
