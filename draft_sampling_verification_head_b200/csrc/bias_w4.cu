@@ -432,9 +432,8 @@ cudaError_t launch_bias_w4(const spec_w4_params& p, const T* x, const int32_t* p
   uint4* xf = reinterpret_cast<uint4*>(body);
   const int wide = x_wide(p, x);
   const int64_t words = (int64_t)p.B * ((p.r + 127) / 128 * 16);
-  k_w4_x<T><<<(unsigned)((words + kThreads - 1) / kThreads), kThreads, 0, st>>>(p, x, prev, xf, NT,
-                                                                               rows, wide, hdr);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_kernel(k_w4_x<T>, (unsigned)((words + kThreads - 1) / kThreads),
+                                      kThreads, 0, st, p, x, prev, xf, NT, rows, wide, hdr);
   if (e != cudaSuccess) return e;
   *launches = 2;
 #define SPEC_W4(NT, G) return product<NT, G>(p, xf, wq, wscale, base, out, rows, parts, num_sms, st)
@@ -456,9 +455,8 @@ cudaError_t launch_bias_w4(const spec_w4_params& p, const T* x, const int32_t* p
 template <typename T>
 cudaError_t launch_w4_quantize(const spec_w4_params& p, const T* W, uint8_t* wq, void* wscale,
                                cudaStream_t st) {
-  k_w4_quantize<T><<<dim3((p.V + kThreads - 1) / kThreads, (p.r + 127) / 128), kThreads, 0, st>>>(
-      p, W, wq, wscale);
-  return cudaGetLastError();
+  return launch_kernel(k_w4_quantize<T>, dim3((p.V + kThreads - 1) / kThreads, (p.r + 127) / 128),
+                       kThreads, 0, st, p, W, wq, wscale);
 }
 
 #define SPEC_INST(T)                                                                               \

@@ -755,8 +755,8 @@ cudaError_t grad(const spec_embed_params& p, const int32_t* ids, const TR* drows
     const int per = zero_rows_per_cta(p, num_sms);
     const int zero = p.accumulate ? 0 : (int)(((int64_t)p.V + per - 1) / per);
     *launches = 1;
-    k_grad_direct<kWide, TT, TR><<<p.n + zero, 32 * kDirectWarps, 0, st>>>(p, ids, drows, dtable, per, hdr);
-    return cudaGetLastError();
+    return launch_kernel(k_grad_direct<kWide, TT, TR>, p.n + zero, 32 * kDirectWarps, 0, st, p, ids,
+                         drows, dtable, per, hdr);
   }
   const GradPlan g = plan_of(p);
   const size_t list = g.keys / 4;
@@ -831,8 +831,7 @@ cudaError_t launch_embed(const spec_embed_params& p, const TT* table, const int3
   *launches = 1;
   const bool wide = wide_ok<TT, TR>(p, table, rows);
   auto run = [&](auto kernel) {
-    kernel<<<(unsigned)grid, kThreads, 0, st>>>(p, table, ids, rows, shift, hdr);
-    return cudaGetLastError();
+    return launch_kernel(kernel, (unsigned)grid, kThreads, 0, st, p, table, ids, rows, shift, hdr);
   };
   if (per == 4) return wide ? run(k_embed<true, 4, TT, TR>) : run(k_embed<false, 4, TT, TR>);
   if (per == 2) return wide ? run(k_embed<true, 2, TT, TR>) : run(k_embed<false, 2, TT, TR>);

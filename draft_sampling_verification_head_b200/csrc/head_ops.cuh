@@ -32,7 +32,20 @@ SPEC_DEV void grid_dependency_release() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// Launch a kernel that calls grid_dependency_wait before it touches anything
+// Launch a kernel and return that launch's own error: the runtime's last one may
+// be an earlier call's.
+template <typename... P, typename... A>
+cudaError_t launch_kernel(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem,
+                          cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
+// The same for a kernel that calls grid_dependency_wait before it touches anything
 // the launch before it writes: its CTAs may be set up while that one ends.
 template <typename... P, typename... A>
 cudaError_t launch_after(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem,

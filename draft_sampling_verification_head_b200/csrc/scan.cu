@@ -878,8 +878,7 @@ cudaError_t by_shape(ScanArgs& a, bool grad, int num_sms, uint8_t* body, cudaStr
   void (*maps)(ScanArgs) = grad ? k_scan_maps<T, V, true> : k_scan_maps<T, V, false>;
   cudaError_t e = allow_smem(maps, sizeof(MapShared<T, V>));
   if (e != cudaSuccess) return e;
-  maps<<<grid, 32 * kSoloWarps, sizeof(MapShared<T, V>), st>>>(a);
-  e = cudaGetLastError();
+  e = launch_kernel(maps, grid, 32 * kSoloWarps, sizeof(MapShared<T, V>), st, a);
   if (e != cudaSuccess) return e;
   *launches = 2;
   return launch<T, V, 1>(a, grad, num_sms, st);

@@ -1184,3 +1184,38 @@ def test_w4_quantize_infinities_and_nan(sdt, wd):
     wqn, sn = sd.w4_quantize(p, W)
     assert torch.equal(wq[3:], wqn[3:]) and torch.equal(s[3:], sn[3:]) and codes[3, 5] == 8
     assert torch.equal(wq[4:], wq0[4:]) and torch.equal(s[4:], s0[4:]) and bool(torch.isfinite(s).all())
+
+
+def test_an_earlier_calls_error_is_not_reported_again():
+    """spec_sync_status on a capturing stream is an error, and stays the runtime's
+    last one; the operators' calls after it launch, and say so."""
+    import ctypes
+    cu = ctypes.CDLL("libcuda.so.1")
+    calls = _every_call(51)
+    big, ids = torch.randn(64, 200, device="cuda"), torch.arange(50, dtype=torch.int32).cuda()
+    pe = sd.EmbedParams(n=50, V=64, D=200, dtype="f32", row_dtype="f32")
+    pl = sd.ScanParams(B=1, T=6000, D=8)
+    we, wl = sd.make_workspace(pe), sd.make_workspace(pl)
+    gate = torch.zeros(1, 6000, 8, dtype=torch.bfloat16, device="cuda")
+    last, out = torch.empty(1, 8, device="cuda"), torch.empty(64, 200, device="cuda")
+    calls += [("embed_grad of few", lambda s: sd.embed_grad(pe, ids, big, out, we, s), [out]),
+              ("split scan", lambda s: sd.gated_scan(pl, gate, gate, None, None, None, last, None, wl, s), [last]),
+              ("quantize", lambda s: sd.w4_quantize(sd.W4Params(B=1, r=64, V=200, group=64), big, s),
+               [])]
+    for _, call, _ in calls:
+        call(None)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for name, call, outs in calls:
+        want = [o.clone() for o in outs]
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        graph, st = ctypes.c_void_p(), ctypes.c_void_p(side.cuda_stream)
+        assert cu.cuStreamBeginCapture_v2(st, 2) == 0  # relaxed
+        assert sd.sync_status(we, side) == sd.SPEC_ERR_CUDA
+        cu.cuStreamEndCapture(st, ctypes.byref(graph))  # invalidated: no graph
+        assert not graph.value
+        call(None)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want)), name
