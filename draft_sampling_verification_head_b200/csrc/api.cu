@@ -46,8 +46,7 @@ EncodeTiledFn encode_fn() {
   if (!fn) {
     void* ptr = nullptr;
     cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) ==
-            cudaSuccess &&
+    if (cuda_ok(cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q)) &&
         q == cudaDriverEntryPointSuccess)
       fn = reinterpret_cast<EncodeTiledFn>(ptr);
   }
@@ -61,10 +60,15 @@ size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 
 }  // namespace
 
+bool cuda_ok(cudaError_t e) {
+  if (e != cudaSuccess) cudaGetLastError();
+  return e == cudaSuccess;
+}
+
 int num_sms() {
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (!cuda_ok(cudaGetDevice(&dev))) return 0;
+  if (!cuda_ok(cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev))) return 0;
   return n;
 }
 
@@ -200,15 +204,14 @@ size_t spec_workspace_size(const spec_params* p) {
 spec_status spec_workspace_init(void* ws, size_t bytes, spec_stream_t stream) {
   if (!ws || bytes < sizeof(WsHeader) || (reinterpret_cast<uintptr_t>(ws) & 255u))
     return SPEC_ERR_WORKSPACE;
-  return cudaMemsetAsync(ws, 0, bytes, (cudaStream_t)stream) == cudaSuccess ? SPEC_OK
-                                                                             : SPEC_ERR_CUDA;
+  return cuda_ok(cudaMemsetAsync(ws, 0, bytes, (cudaStream_t)stream)) ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
 spec_status spec_sync_status(const void* ws, spec_stream_t stream) {
   if (!ws) return SPEC_ERR_WORKSPACE;
-  if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return SPEC_ERR_CUDA;
+  if (!cuda_ok(cudaStreamSynchronize((cudaStream_t)stream))) return SPEC_ERR_CUDA;
   int32_t st = 0;
-  if (cudaMemcpy(&st, ws, sizeof(st), cudaMemcpyDeviceToHost) != cudaSuccess) return SPEC_ERR_CUDA;
+  if (!cuda_ok(cudaMemcpy(&st, ws, sizeof(st), cudaMemcpyDeviceToHost))) return SPEC_ERR_CUDA;
   return (spec_status)st;
 }
 
@@ -237,7 +240,7 @@ spec_status spec_markov_bias(const spec_params* p, const void* U, const void* W,
                         bias, p->B, p->V, p->r, header_of(ws), st);
   }
   g_last_launches = 1;
-  return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+  return cuda_ok(e) ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
 // The fused cycle on the tensor-core path (geometry already decided).
@@ -293,7 +296,7 @@ static spec_status run_cycle_tc(const spec_params* p, const CycleGeom& g, const 
   L.trace = (p->flags & SPEC_FLAG_TRACE) != 0;
   cudaError_t e = launch_cycle_tc(L, g, header_of(ws), body_of(ws), &tmW, (cudaStream_t)stream);
   g_last_launches = 1;
-  if (e != cudaSuccess) {
+  if (!cuda_ok(e)) {
     fprintf(stderr, "specdec: launch failed: %s\n", cudaGetErrorString(e));
     return SPEC_ERR_CUDA;
   }
@@ -364,7 +367,7 @@ static spec_status run_cycle(const spec_params* p, int mode, const void* base, c
   cudaError_t e = launch_cycle(L, g, header_of(ws), body_of(ws), g.tc ? &tmW : nullptr, &tmBase,
                                (cudaStream_t)stream);
   g_last_launches = 1;
-  if (e != cudaSuccess) {
+  if (!cuda_ok(e)) {
     fprintf(stderr, "specdec: launch failed: %s\n", cudaGetErrorString(e));
     return SPEC_ERR_CUDA;
   }
@@ -471,7 +474,7 @@ static spec_status run_verify(const spec_params* p, const void* target, const vo
     e = verify_dispatch<float, float>(p, target, draft_logits, draft, vlen, out, tau, p_draft,
                                       q_draft, fused, body, h, sms, st, &launches);
   g_last_launches = launches;
-  if (e != cudaSuccess) {
+  if (!cuda_ok(e)) {
     fprintf(stderr, "specdec: launch failed: %s\n", cudaGetErrorString(e));
     return SPEC_ERR_CUDA;
   }
@@ -527,25 +530,25 @@ spec_status spec_l2_persist(const void* ptr, size_t bytes, spec_stream_t stream)
   memset(&v, 0, sizeof(v));
   if (bytes == 0 || ptr == nullptr) {
     v.accessPolicyWindow.num_bytes = 0;
-    if (cudaStreamSetAttribute(st, cudaStreamAttributeAccessPolicyWindow, &v) != cudaSuccess)
+    if (!cuda_ok(cudaStreamSetAttribute(st, cudaStreamAttributeAccessPolicyWindow, &v)))
       return SPEC_ERR_CUDA;
-    return cudaCtxResetPersistingL2Cache() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+    return cuda_ok(cudaCtxResetPersistingL2Cache()) ? SPEC_OK : SPEC_ERR_CUDA;
   }
   int dev = 0, max_persist = 0, max_window = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&max_persist, cudaDevAttrMaxPersistingL2CacheSize, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&max_window, cudaDevAttrMaxAccessPolicyWindowSize, dev) != cudaSuccess)
+  if (!cuda_ok(cudaGetDevice(&dev)) ||
+      !cuda_ok(cudaDeviceGetAttribute(&max_persist, cudaDevAttrMaxPersistingL2CacheSize, dev)) ||
+      !cuda_ok(cudaDeviceGetAttribute(&max_window, cudaDevAttrMaxAccessPolicyWindowSize, dev)))
     return SPEC_ERR_CUDA;
   if (max_persist <= 0 || max_window <= 0) return SPEC_ERR_UNSUPPORTED;
   const size_t window = std::min(bytes, (size_t)max_window);
   const size_t carve = std::min(window, (size_t)max_persist);
-  if (cudaDeviceSetLimit(cudaLimitPersistingL2CacheSize, carve) != cudaSuccess) return SPEC_ERR_CUDA;
+  if (!cuda_ok(cudaDeviceSetLimit(cudaLimitPersistingL2CacheSize, carve))) return SPEC_ERR_CUDA;
   v.accessPolicyWindow.base_ptr = const_cast<void*>(ptr);
   v.accessPolicyWindow.num_bytes = window;
   v.accessPolicyWindow.hitRatio = (float)carve / (float)window;
   v.accessPolicyWindow.hitProp = cudaAccessPropertyPersisting;
   v.accessPolicyWindow.missProp = cudaAccessPropertyStreaming;
-  return cudaStreamSetAttribute(st, cudaStreamAttributeAccessPolicyWindow, &v) == cudaSuccess
+  return cuda_ok(cudaStreamSetAttribute(st, cudaStreamAttributeAccessPolicyWindow, &v))
              ? SPEC_OK
              : SPEC_ERR_CUDA;
 }
@@ -554,16 +557,15 @@ spec_status spec_debug_philox(const uint32_t* ctr, const uint32_t* key, uint32_t
                               spec_stream_t stream) {
   if (!ctr || !key || !out || n < 0) return SPEC_ERR_INVALID_ARG;
   if (n == 0) return SPEC_OK;
-  return launch_debug_philox(ctr, key, out, n, (cudaStream_t)stream) == cudaSuccess
-             ? SPEC_OK
-             : SPEC_ERR_CUDA;
+  return cuda_ok(launch_debug_philox(ctr, key, out, n, (cudaStream_t)stream)) ? SPEC_OK
+                                                                              : SPEC_ERR_CUDA;
 }
 
 spec_status spec_debug_curand_philox(const uint32_t* ctr, const uint32_t* key, uint32_t* out,
                                      int32_t n, spec_stream_t stream) {
   if (!ctr || !key || !out || n < 0) return SPEC_ERR_INVALID_ARG;
   if (n == 0) return SPEC_OK;
-  return launch_debug_curand_philox(ctr, key, out, n, (cudaStream_t)stream) == cudaSuccess
+  return cuda_ok(launch_debug_curand_philox(ctr, key, out, n, (cudaStream_t)stream))
              ? SPEC_OK
              : SPEC_ERR_CUDA;
 }

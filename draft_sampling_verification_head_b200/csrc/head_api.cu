@@ -30,8 +30,7 @@ uint8_t* body_of(void* ws) { return reinterpret_cast<uint8_t*>(ws) + sizeof(WsHe
 
 spec_status launched(cudaError_t e, int launches) {
   g_last_launches = launches;
-  if (e == cudaSuccess) return SPEC_OK;
-  cudaGetLastError();  // reported here, and not by the next call as well
+  if (cuda_ok(e)) return SPEC_OK;
   fprintf(stderr, "specdec: launch failed: %s\n", cudaGetErrorString(e));
   return SPEC_ERR_CUDA;
 }

@@ -9,6 +9,9 @@ namespace specdec {
 // ---- Shared by the entry points (api.cu) ------------------------------------------
 extern thread_local int32_t g_last_launches;  // kernel launches of the thread's last call
 int num_sms();                                // SMs of the current device, 0 on an error
+// Whether a runtime call succeeded.  An error is taken off the runtime's last one:
+// the call that met it reports it, and no later launch must.
+bool cuda_ok(cudaError_t e);
 
 // Record a device-side error of an operator: the first one stays.  Unlike
 // record_error this leaves the abort flag alone, which ends the waits of the

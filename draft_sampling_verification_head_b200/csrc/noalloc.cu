@@ -16,6 +16,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "head_ops.cuh"
 #include "specdec.h"
 
 namespace {
@@ -42,9 +43,9 @@ unsigned long long current_context_id() {
     void* f1 = nullptr;
     void* f2 = nullptr;
     cudaDriverEntryPointQueryResult q1, q2;
-    if (cudaGetDriverEntryPoint("cuCtxGetCurrent", &f1, cudaEnableDefault, &q1) == cudaSuccess &&
+    if (specdec::cuda_ok(cudaGetDriverEntryPoint("cuCtxGetCurrent", &f1, cudaEnableDefault, &q1)) &&
         q1 == cudaDriverEntryPointSuccess &&
-        cudaGetDriverEntryPoint("cuCtxGetId", &f2, cudaEnableDefault, &q2) == cudaSuccess &&
+        specdec::cuda_ok(cudaGetDriverEntryPoint("cuCtxGetId", &f2, cudaEnableDefault, &q2)) &&
         q2 == cudaDriverEntryPointSuccess) {
       get_current = reinterpret_cast<GetCurrentFn>(f1);
       get_id = reinterpret_cast<GetIdFn>(f2);
@@ -65,7 +66,7 @@ unsigned long long current_context_id() {
 // array's name is only a host-side stand-in, never a device address.
 void* scratch_for_current_device(spec_status* err) {
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+  if (!specdec::cuda_ok(cudaGetDevice(&dev)) || dev < 0 || dev >= kMaxDevices) {
     *err = SPEC_ERR_CUDA;
     return nullptr;
   }
@@ -73,7 +74,7 @@ void* scratch_for_current_device(spec_status* err) {
   const unsigned long long ctx = current_context_id();
   if (!g_scratch_addr[dev] || (ctx != 0 && ctx != g_scratch_ctx[dev])) {
     void* p = nullptr;
-    if (cudaGetSymbolAddress(&p, g_noalloc_scratch) != cudaSuccess || !p) {
+    if (!specdec::cuda_ok(cudaGetSymbolAddress(&p, g_noalloc_scratch)) || !p) {
       *err = SPEC_ERR_CUDA;
       return nullptr;
     }
@@ -108,13 +109,13 @@ extern "C" spec_status spec_cycle_noalloc(const spec_params* p, const void* base
   // The header's last word (the count of earlier step events, which keeps the
   // record tags of consecutive calls apart) is kept; the rest of the scratch
   // needs no clearing: a launch writes every entry before reading it.
-  if (cudaMemsetAsync(ws, 0, sizeof(specdec::WsHeader) - sizeof(uint32_t), st) != cudaSuccess)
+  if (!specdec::cuda_ok(cudaMemsetAsync(ws, 0, sizeof(specdec::WsHeader) - sizeof(uint32_t), st)))
     return SPEC_ERR_CUDA;
   const spec_status s = spec_cycle(p, base, target, U, W, last_token, draft, out, tau, p_draft,
                                    q_draft, ws, stream);
   if (s != SPEC_OK) return s;
   if (status_out &&
-      cudaMemcpyAsync(status_out, ws, sizeof(int32_t), cudaMemcpyDeviceToDevice, st) != cudaSuccess)
+      !specdec::cuda_ok(cudaMemcpyAsync(status_out, ws, sizeof(int32_t), cudaMemcpyDeviceToDevice, st)))
     return SPEC_ERR_CUDA;
   return SPEC_OK;
 }

@@ -1187,8 +1187,8 @@ def test_w4_quantize_infinities_and_nan(sdt, wd):
 
 
 def test_an_earlier_calls_error_is_not_reported_again():
-    """spec_sync_status on a capturing stream is an error, and stays the runtime's
-    last one; the operators' calls after it launch, and say so."""
+    """spec_sync_status on a capturing stream is an error; the calls after it launch,
+    and say so, the operators' and the other ones."""
     import ctypes
     cu = ctypes.CDLL("libcuda.so.1")
     calls = _every_call(51)
@@ -1202,11 +1202,25 @@ def test_an_earlier_calls_error_is_not_reported_again():
               ("split scan", lambda s: sd.gated_scan(pl, gate, gate, None, None, None, last, None, wl, s), [last]),
               ("quantize", lambda s: sd.w4_quantize(sd.W4Params(B=1, r=64, V=200, group=64), big, s),
                [])]
+    f = torch.randn(4200, 64, device="cuda")
+    d, bias = torch.zeros(4200, 1, dtype=torch.int32, device="cuda"), torch.zeros(4200, 64, device="cuda")
+    ctr = torch.arange(64, dtype=torch.int32, device="cuda").view(8, 8)
+    ph, tau, vo = torch.zeros(8, 4, dtype=torch.int32, device="cuda"), torch.zeros_like(d[:, 0]), torch.zeros_like(d)
+    vo = vo.expand(-1, 2).contiguous()
+    pf, pb = (sd.Params(B=4200, K=1, V=64, r=64, dtype=t, draft_dtype="f32") for t in ("f32", "bf16"))
+    wf, wb = sd.make_workspace(pf), sd.make_workspace(pb)
+    b16 = f.bfloat16()
+    calls += [("philox", lambda s: sd.debug_philox(ctr[:, :4].contiguous(), ctr[:, 4:6].contiguous(), ph, s), [ph]),
+              ("bias f32", lambda s: sd.markov_bias(pf, f[:64], f[64:128], d[:, 0], bias, wf, s), [bias]),
+              ("bias bf16", lambda s: sd.markov_bias(pb, b16[:64], b16[64:128], d[:, 0], bias, wb, s), [bias]),
+              ("verify", lambda s: sd.verify_block(pf, f.repeat(2, 1), f, d, vo, tau, None, None, wf, s), [vo, tau])]
     for _, call, _ in calls:
         call(None)
     torch.cuda.synchronize()
+    torch.cuda.synchronize()
     side = torch.cuda.Stream()
     for name, call, outs in calls:
+        call(None)
         want = [o.clone() for o in outs]
         for o in outs:
             o.zero_()
