@@ -20,7 +20,9 @@ SPEC_DEV void store_any(void* p, int32_t dtype, int64_t i, float v) {
     store_f((float*)p, i, v);
 }
 
-// Eight codes as four pairs (k, k + 4) of bf16.
+// Eight codes as four pairs (k, k + 4) of bf16.  A bf16 has 7 fraction bits, so from
+// 128 to 256 its steps are 1: 0x4300 is 128, 0x4300 | code is 128 + code, and taking
+// 136 (0x4308) off is exact and leaves code - 8.
 SPEC_DEV void codes_to_bf16(uint32_t w, uint32_t* p) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -95,29 +97,21 @@ struct XWord {
   }
 };
 
-
 // Rows of X on 16-byte boundaries.
 template <typename T>
 bool x_wide(const spec_w4_params& p, const T* x) {
   return (reinterpret_cast<uintptr_t>(x) & 15) == 0 && p.x_stride * sizeof(T) % 16 == 0;
 }
 
-// Byte of features k, k + 1 (k even) inside a packed row.
-__host__ __device__ __forceinline__ int packed_byte(int k) {
-  const int w = (k & 127) >> 3;  // word of eight features
-  return (k >> 7) * 64 + (4 * (w & 3) + (w >> 2)) * 4 + ((k & 7) >> 1);
-}
-
 // ----------------------------------------------------------------------------
-// The product.  A warp multiplies MT tiles of 16 tokens by up to 8 NT columns of
-// X on the tensor cores (m16n8k16, bf16 in, fp32 out).  Codes become bf16
-// exactly (0x4300 | code is 128 + code, less 136); a lane's 16 bytes of a row
-// hold one word of each 32 features, so the multiply of a group needs no other
-// lane's bytes, and the order of the features inside a word is given to X instead
-// (a nibble and the one 16 bits above it make a pair).  The sum of a group stays
-// in the accumulator, is scaled in fp32 and added to the row's.  fp32 X is cut
-// into three bf16 parts, which together hold all its 24 bits, as columns of
-// their own, so its products are exact as well.
+// The product.  A warp multiplies kTiles tiles of 16 tokens by up to 8 NT columns
+// of X on the tensor cores (m16n8k16, bf16 in, fp32 out).  Codes become bf16
+// exactly; a lane's 16 bytes of a row hold one word of each 32 features, so the
+// multiply of a group needs no other lane's bytes, and the order of the features
+// inside a word is given to X instead (a nibble and the one 16 bits above it make
+// a pair).  The sum of a group stays in the accumulator, is scaled in fp32 and
+// added to the row's.  fp32 X is cut into three bf16 parts, which together hold
+// all its 24 bits, as columns of their own, so its products are exact as well.
 //
 // The codes pass through once, two blocks of 128 features ahead of the products
 // in registers; that is their floor in bytes.  X is laid out beforehand (k_w4_x) as the

@@ -731,7 +731,8 @@ GradPlan plan_of(const spec_embed_params& p) {
   while (g.lanes < 32 && g.lanes * kCols < p.D) g.lanes *= 2;
   g.blocks = (p.D + g.lanes * kCols - 1) / (g.lanes * kCols);
   g.width = g.blocks * g.lanes * kCols;
-  // enough pieces to fill the GPU, long enough to be worth their parts
+  // enough pieces to fill the GPU, long enough to be worth their parts; of a B200's
+  // size on any device, so that the workspace's size is the same on all
   g.piece = 16;
   while (g.piece < 128 && (int64_t)p.n / (2 * g.piece) * g.blocks * g.lanes >= 148 * 384) g.piece *= 2;
   g.pieces = (int)(((int64_t)p.n + g.piece - 1) / g.piece);

@@ -6,9 +6,11 @@
 // are dealt to the warps in contiguous chunks, whose masses are summed in 64 bits
 // and sent to all CTAs of the cluster.  Each warp sees from the chunks' sums
 // whether the drawn token lies in its own; the one that holds it reads its chunk
-// again (from L2) and finds the token.  Summing in 64 bits is what lets the token
-// be independent of the order: the fp32 terms are exact in it, and a token's
-// border would have to lie within 2^-52 of the draw to be decided otherwise.
+// again (from L2) and finds the token.  The order of these 64-bit sums is fixed by
+// the sizes and the device.  A sum of n terms, none negative, each rounded once, is
+// off by at most n 2^-53 of itself in any order; so are the total and the mass up to
+// a token, and another order can only decide otherwise where the draw lies within
+// (n + 2) 2^-52 of the total of the token's border (n = 151936: 3.4e-11).
 //
 // What bounds it: the rows' bytes, behind a chain of dependent reads (lengths,
 // drafts, their probabilities, the row, the chunk again) that a row's CTAs go

@@ -472,11 +472,11 @@ typedef struct {
  * The draw takes the first token whose inclusive mass exceeds u_draw * total
  * (else the last one with mass), in ascending token order, from max(p_j - q_j, 0)
  * at the first rejection j (p_j where that has no mass), or from p_{K_b}.
- * Masses are summed in 64 bits, so the token does not hang on the order of the
- * sums.  A p that is NaN, infinite or negative has no mass; a q that is NaN or
- * negative counts as 0.  A row
- * without any mass emits -1 there, has tau = the number of accepted drafts,
- * and is reported as SPEC_ERR_INVALID_ARG.  A draft outside [0, V) is rejected
+ * Masses are summed in 64 bits: the order of the sums can decide only where
+ * u_draw * total lies within (V + 2) 2^-52 of the total of a token's border.
+ * A p that is NaN, infinite or negative has no mass; a q that is NaN or
+ * negative counts as 0.  A row without any mass emits -1 there, has tau = the
+ * number of accepted drafts, and is reported as SPEC_ERR_INVALID_ARG.  A draft outside [0, V) is rejected
  * and reported as SPEC_ERR_TOKEN_RANGE.  Only the rows of the first rejection
  * (or the bonus row) are read whole. */
 spec_status spec_verify_probs(const spec_probs_params *p, const void *target,
