@@ -469,8 +469,8 @@ __global__ void __launch_bounds__(kSortThreads) k_grad_sort(SortArgs a) {
     __threadfence();
     const uint32_t left = atomicAdd(&a.hdr->exit_count, ok ? 1u : 0x10001u);
     if ((left & 0xFFFFu) == (uint32_t)a.ctas - 1) {
-      __threadfence();
       gave_up = !ok || left >> 16;
+      if (gave_up) __threadfence();  // the list is written after what the others wrote
       a.hdr->bar = 0;
       a.hdr->abort = 0;
       a.hdr->exit_count = 0;

@@ -265,6 +265,7 @@ struct Joiner {
   float2 piece[2][W][32 * V];
   float2 cta[2][kMaxCluster][32 * V];
   uint64_t full[2];
+  volatile int gave_up[2];  // by a window's parity: a wait of it ran out
 };
 template <int V>
 struct Joiner<V, 1> {
@@ -281,6 +282,7 @@ SPEC_DEV void join_init(Joiner<V, W>& sm, int cluster) {
     if (threadIdx.x == 0) {
       mbar_init(&sm.full[0], 1);
       mbar_init(&sm.full[1], 1);
+      sm.gave_up[0] = sm.gave_up[1] = 0;
       fence_mbar_init();
     }
     cg::this_cluster().sync();  // every CTA runs, its barriers ready, before another writes to it
@@ -317,18 +319,24 @@ SPEC_DEV bool cluster_wait(uint64_t* bar, uint32_t parity, uint64_t polls) {
 // The end of a CTA in which a wait ran out: others may still send to its shared
 // memory, so it stays until their threads have ended or wait here as well (which
 // they do, as their own waits are bounded) and what they sent has arrived.
-SPEC_DEV void cluster_give_up() {
-  cp_async_wait<0>();
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-  __nanosleep(1000000);
+template <int V, int W>
+SPEC_DEV void join_end(Joiner<V, W>& sm, int cluster) {
+  if constexpr (W > 1) {
+    if (cluster == 1 || !(sm.gave_up[0] | sm.gave_up[1])) return;
+    cp_async_wait<0>();
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+    __nanosleep(1000000);
+  }
 }
 
-// Returns false where the CTA has to leave: a wait of one of its threads ran out
-// in the window before (`ok` of that thread is false).  It sends and arrives no
-// more then, since its barriers' phases are no longer the others'.
+// Returns false where the CTA has to leave, all of its threads alike: a wait of one
+// of them ran out in the window before.  It sends and arrives no more then, since
+// its barriers' phases are no longer the others', who give up in turn.  (The flag
+// in shared memory costs the gradient of 8 x 8192 x 1024 4 % against no way out; as
+// the window barrier's own reduction 5 %, kept by each thread 7 %.)
 template <int V, int W>
 SPEC_DEV bool join(Joiner<V, W>& sm, int win, int warp, int rank, int cluster, Vec<V> a, Vec<V> c,
-                   Vec<V>& carry, Vec<V>& before, bool& ok, uint64_t polls, WsHeader* hdr) {
+                   Vec<V>& carry, Vec<V>& before, uint64_t polls, WsHeader* hdr) {
   const int par = win & 1;
   if constexpr (W == 1) {
     before = carry;
@@ -338,10 +346,8 @@ SPEC_DEV bool join(Joiner<V, W>& sm, int win, int warp, int rank, int cluster, V
 #pragma unroll
     for (int v = 0; v < V; ++v)
       sm.piece[par][warp][v * 32 + lane] = make_float2(a.get(v), c.get(v));
-    if (__syncthreads_or(!ok)) {
-      ok = false;
-      return false;
-    }
+    __syncthreads();
+    if (cluster > 1 && sm.gave_up[par ^ 1]) return false;
     float out_b[V], out_c[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -372,8 +378,10 @@ SPEC_DEV bool join(Joiner<V, W>& sm, int win, int warp, int rank, int cluster, V
     if (cluster > 1) {
       if (threadIdx.x == 0)
         mbar_arrive_expect_tx(&sm.full[par], (uint32_t)(cluster * 32 * V * sizeof(float2)));
-      ok = cluster_wait(&sm.full[par], (win >> 1) & 1, polls);
-      if (!ok) report_error(hdr, SPEC_ERR_TIMEOUT, SITE_MBAR_FULL, rank, win);
+      if (!cluster_wait(&sm.full[par], (win >> 1) & 1, polls)) {
+        sm.gave_up[par] = 1;
+        report_error(hdr, SPEC_ERR_TIMEOUT, SITE_MBAR_FULL, rank, win);
+      }
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         float s = carry.get(v), mine = s;
@@ -505,7 +513,6 @@ __global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), 2)
     }
   }
   const int nwin = (at.t1 - at.t0 + window - 1) / window;
-  bool ok = true;
   for (int win = 0, stage = 0; win < nwin; ++win, t0 += window) {
     Vec<V> f[kChunk], z[kChunk], ma = Vec<V>::all(1.f), mc = Vec<V>::all(0.f);
     cp_async_wait<kStages - 1>();
@@ -534,7 +541,7 @@ __global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), 2)
     request(t0 + kStages * window, stage);
     stage ^= 1;
     Vec<V> s;
-    if (!join<V, W>(sm.joiner, win, warp, rank, C, ma, mc, carry, s, ok, a.polls, a.hdr)) break;
+    if (!join<V, W>(sm.joiner, win, warp, rank, C, ma, mc, carry, s, a.polls, a.hdr)) break;
     if (on && a.states && t0 < Tn)
       state_store<V>(a.states + ((int64_t)b * nch + t0 / kChunk) * D + c, s);
     if (on && a.h && left > 0) {
@@ -558,7 +565,7 @@ __global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), 2)
   }
   if (a.h_last && at.pos == a.nseg - 1 && rank == 0 && warp == 0 && on)
     state_store<V>(a.h_last + (int64_t)b * D + c, carry);
-  if (W > 1 && !ok) cluster_give_up();
+  join_end<V, W>(sm.joiner, C);
 }
 
 // Gradient.  The state before each piece comes from `states`, so its h are run
@@ -619,7 +626,6 @@ __global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), 2)
     }
   }
   const int nwin = (ch1 - ch0 + window - 1) / window;
-  bool ok = true;
   for (int win = 0; win < nwin; ++win, ch -= window) {
     const int t0 = ch * kChunk, left = ch < ch0 ? 0 : n - t0, par = win & 1;
     Vec<V> f[kChunk], i[kChunk], w[kChunk], ma = Vec<V>::all(1.f), mc = Vec<V>::all(0.f);
@@ -650,7 +656,7 @@ __global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), 2)
     ma = ma.map(above_zero);
     __syncwarp();
     request(ch - window, par ^ 1);
-    if (!join<V, W>(sm.joiner, win, warp, rank, C, ma, mc, carry, s, ok, a.polls, a.hdr)) break;
+    if (!join<V, W>(sm.joiner, win, warp, rank, C, ma, mc, carry, s, a.polls, a.hdr)) break;
     if (on && ch >= ch0) {
       T* dg = dgp + (int64_t)t0 * a.p.gate_stride;
       T* dx = dxp + (int64_t)t0 * a.p.x_stride;
@@ -681,7 +687,7 @@ __global__ void __launch_bounds__(32 * (W == 1 ? kSoloWarps : W), 2)
   }
   if (a.dh0 && at.pos == a.nseg - 1 && rank == 0 && warp == 0 && on)
     state_store<V>(a.dh0 + (int64_t)b * D + c, carry);
-  if (W > 1 && !ok) cluster_give_up();
+  join_end<V, W>(sm.joiner, C);
 }
 
 // ----------------------------------------------------------------------------
