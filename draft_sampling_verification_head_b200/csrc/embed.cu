@@ -109,11 +109,12 @@ SPEC_DEV void store8(T* p, const Columns<kWide>& c, const float* x) {
 // rows[i] = scale * table[ids[i]].  `lanes` lanes take one row of four blocks of
 // columns at a time, or kRows rows of 4 / kRows blocks, so that four blocks' loads
 // are in flight together (single columns, which cost eight loads a block, take one
-// block of each row).  Bytes bound it: the named rows of the table in, the rows out,
-// though repeated rows come from L2, whose traffic (every row in, every row out)
-// is then the limit: 65536 rows of 1024 fp32 to bf16 in 39 us, 4.4 TB/s of the
-// distinct bytes and 10 TB/s of all.  One row at a time instead: rows of 256 bf16 in
-// 30 us against 17, of 512 in 33 against 23.
+// block of each row).  Bytes bound it: the named rows of the table in, the rows out.
+// Repeated rows come from the caches (65536 rows of 1024 fp32 to bf16 by Zipf's
+// tokens: 39 % of what is read from L1, 42 % from L2, the rest from memory), and the
+// traffic of L2, 163 MB in and 134 MB out at 8 TB/s, is then the limit: 40 us, 4.4
+// TB/s of the distinct bytes.  One row at a time instead: rows of 256 bf16 in 30 us
+// against 17, of 512 in 33 against 23.
 template <bool kWide, int kRows, typename TT, typename TR>
 __global__ void __launch_bounds__(kThreads, kWide ? 1 : 4)
     k_embed(spec_embed_params p, const TT* __restrict__ table, const int32_t* __restrict__ ids,
